@@ -77,9 +77,10 @@ typedef enum {
                        quantised on the fly from bf16 to MXFP8 (E4M3 + E8M0 per 32) and
                        multiplied with gfx950's scaled MFMA (W4A8).  latent and inter must be
                        multiples of 128 (else MOE_EUNSUPPORTED) */
-  MOE_MXFP4_A4 = 4  /* as MOE_MXFP4_A8 with z and h quantised to MXFP4 (E2M1 + E8M0 per 32,
+  MOE_MXFP4_A4 = 4, /* as MOE_MXFP4_A8 with z and h quantised to MXFP4 (E2M1 + E8M0 per 32,
                        shared exponent floor(log2 amax) - 2): W4A4 on the scaled MFMA with
                        E2M1 on both operands; same size limits */
+  MOE_F16 = 5       /* IEEE half: inputs and outputs of the MXFP4 packing and products only */
 } moe_dtype;
 
 typedef enum {
@@ -387,6 +388,173 @@ int moe_latent_backward_train(const moe_shape_t* shape, const moe_weights_t* wei
                               const void* dout, const void* saved, size_t saved_bytes,
                               const moe_grads_t* grads, int apply_sgd, float lr, void* workspace,
                               size_t workspace_bytes, void* stream);
+
+/*
+ * The balance loss of the router, per sequence, with per-expert counts: the
+ * auxiliary loss that Quantile Balancing makes unnecessary, for training a
+ * router without it (or beside it), as the fixed-step sign update above is.
+ * Over the counted tokens t of sequence s (N of them), with p_ti = s_ti /
+ * sum_j s_tj the shares of the token's scores and c_i the number of times
+ * expert i was chosen,
+ *     loss_s = n / (k N^2) * sum_i c_i sum_t p_ti        (1 for even counts)
+ * and, the choices held fixed,
+ *     d loss_s / d s_tj = n / (k N^2) * (c_j - sum_i c_i p_ti) / sum_i s_ti.
+ * A sequence without counted tokens has loss 0; a token whose scores sum to 0
+ * has no shares and a zero gradient.
+ *
+ *   scores   [T][n] f32 >= 0, rows ld_scores elements apart (>= n), n <= 1024
+ *   topk_idx [T][k] i32, the choices (contiguous).  An index outside [0, n)
+ *            counts nowhere (a dropped choice may be written as -1)
+ *   seq_offsets [n_seq + 1] i32, non-decreasing: sequence s holds tokens
+ *            [seq_offsets[s], seq_offsets[s + 1]); NULL with n_seq = 1: the
+ *            whole batch.  Tokens outside every sequence are not counted
+ *   token_mask [T] u8 or NULL: tokens with 0 (padding) are not counted, and
+ *            their scores are not read
+ *   dloss    [n_seq] f32 or NULL (ones): the gradient of each loss_s, applied
+ *            to dscores; loss itself is not scaled
+ *   loss     [n_seq] f32; counts [n_seq][n] i32; tokens [n_seq] i32 (N)
+ *   dscores  [T][n] f32 or NULL: when given, the gradient comes out of the
+ *            same pass over the scores.  Rows of tokens that are not counted
+ *            are zero.  May not overlap the inputs
+ *   workspace: >= moe_balance_loss_workspace_bytes(T, n_seq) bytes, 256-byte
+ *            aligned
+ * Results do not depend on the order in which blocks run.
+ */
+size_t moe_balance_loss_workspace_bytes(int32_t T, int32_t n_seq);
+
+int moe_balance_loss(const float* scores, int64_t ld_scores, int32_t T, int32_t n, int32_t k,
+                     const int32_t* topk_idx, const int32_t* seq_offsets, int32_t n_seq,
+                     const uint8_t* token_mask, const float* dloss, float* loss, int32_t* counts,
+                     int32_t* tokens, float* dscores, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/* moe_balance_loss_backward -- the gradient alone, from the counts and tokens
+ * that moe_balance_loss returned; the same bits as its dscores. */
+int moe_balance_loss_backward(const float* scores, int64_t ld_scores, int32_t T, int32_t n,
+                              int32_t k, const int32_t* counts, const int32_t* tokens,
+                              const int32_t* seq_offsets, int32_t n_seq,
+                              const uint8_t* token_mask, const float* dloss, float* dscores,
+                              void* stream);
+
+/*
+ * moe_router_backward -- a gradient of all the router's scores taken to what
+ * made them: scores = sigmoid(x W_r^T + offset), g = dscores * s * (1 - s),
+ *     dx = g W_r,   d_w_router = g^T x,   d_router_logit_offset = sum_t g.
+ * (moe_latent_backward's own gradient reaches the router through the chosen
+ * scores only; a loss on all scores, as the balance loss, comes in here.)
+ *   x [T][d] bf16, w_router [n][d] f32, scores and dscores [T][n] f32
+ *            (contiguous); d a multiple of 64, n <= 1024
+ *   accumulate 0: outputs are overwritten; 1: added to (dx = bf16(dx + .),
+ *            the others in fp32), for gradients moe_latent_backward wrote
+ *   dx [T][d] bf16, d_w_router [n][d] f32, d_router_logit_offset [n] f32;
+ *            each may be NULL
+ *   workspace: >= moe_router_backward_workspace_bytes(T, d, n) bytes, 256-byte
+ *            aligned
+ * The products run on the bf16 MFMA with fp32 accumulation: d_w_router from
+ * the exact split of g into three bf16 parts, dx (a bf16 output) from two parts
+ * of g and of W_r.  Deterministic.
+ */
+size_t moe_router_backward_workspace_bytes(int32_t T, int32_t d, int32_t n);
+
+int moe_router_backward(const void* x, const float* w_router, const float* scores,
+                        const float* dscores, int32_t T, int32_t d, int32_t n, int accumulate,
+                        void* dx, float* d_w_router, float* d_router_logit_offset,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_mxfp4_pack -- MXFP4 rounding of a matrix, or a batch of them, along its
+ * rows, along its columns, or both from one read.
+ *   x        [batch][rows][cols], dtype MOE_F32, MOE_BF16 or MOE_F16; rows are
+ *            row_stride and matrices batch_stride elements apart
+ *   codes    [batch][rows][cb * 16] u8 and scales [batch][rows][cb] u8, cb =
+ *            ceil(cols / 32), or both NULL: blocks of 32 along each row, the
+ *            last one filled up with zeros (the layout of moe_mxfp4_quantize)
+ *   codes_t  [batch][cols][rb * 16] u8 and scales_t [batch][cols][rb] u8, rb =
+ *            moe_mxfp4_padded_rows(rows, n_groups) / 32, or both NULL: blocks
+ *            of 32 along each column, written transposed: the operand of a
+ *            product that contracts over the rows
+ *   row_offsets [n_groups + 1] i32, non-decreasing, or NULL with n_groups = 0
+ *            (n_groups <= 1024, batch 1, with codes_t): the rows are those of
+ *            groups (experts), and no block of a column crosses from one to the
+ *            next: group g starts at padded row padded_offsets[g], a multiple
+ *            of 32, its last block filled up with zeros.  Rows outside every
+ *            group are neither read nor written
+ *   padded_offsets [n_groups + 1] i32, written (the k_offsets of
+ *            moe_mxfp4_matmul_kgroup)
+ * Scale exponent floor(log2 amax) - 2 clamped to [-127, 127], elements to the
+ * nearest E2M1 value, ties to the even code, at most 6 in magnitude, as
+ * moe_mxfp4_quantize, and the same codes for finite inputs.  A block that
+ * holds an infinity or NaN gets scale byte 255 (NaN) and codes 0.  codes and
+ * codes_t 16-byte aligned; x aligned to its elements.
+ */
+int64_t moe_mxfp4_padded_rows(int64_t rows, int32_t n_groups);
+
+int moe_mxfp4_pack(const void* x, int32_t dtype, int64_t batch, int64_t rows, int64_t cols,
+                   int64_t row_stride, int64_t batch_stride, uint8_t* codes, uint8_t* scales,
+                   uint8_t* codes_t, uint8_t* scales_t, const int32_t* row_offsets,
+                   int32_t n_groups, int32_t* padded_offsets, void* stream);
+
+/* moe_mxfp4_unpack -- the values of packed rows: codes [rows][cb * 16], scales
+ * [rows][cb], cb = ceil(cols / 32), to out [rows][cols] of MOE_F32, MOE_BF16
+ * (both hold every value exactly) or MOE_F16 (rounded), rows row_stride
+ * elements apart.  Scale byte 255 gives NaN. */
+int moe_mxfp4_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                     int32_t dtype, void* out, int64_t row_stride, void* stream);
+
+/*
+ * moe_mxfp4_matmul -- C = A B^T of MXFP4 operands on the scaled MFMA, fp32
+ * accumulation.
+ *   a_codes  [a_rows][K/2], a_scales [a_rows][K/32]; b_codes [n_groups][N][K/2],
+ *            b_scales [n_groups][N][K/32] (the routed experts' weights as
+ *            moe_weights_t holds them); K a multiple of 32 (operands packed from
+ *            other widths are filled up to one); codes 16-byte aligned
+ *   row_offsets NULL (n_groups = 1): one product of M rows.  Else [n_groups + 1]
+ *            i32, non-decreasing, n_groups <= 1024: rows [row_offsets[g],
+ *            row_offsets[g + 1]) of C meet matrix g.  Rows of C outside every
+ *            group are left as they were
+ *   row_index [M] i32 or NULL: row r of C is made from row row_index[r] of A
+ *            (an index outside [0, a_rows) stands for a row of zeros); NULL: row r
+ *   out      [M][N] of out_dtype (MOE_F32, MOE_BF16, MOE_F16), rows ld_out
+ *            elements apart, rounded once from the fp32 sum
+ */
+int moe_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t a_rows,
+                     const uint8_t* b_codes, const uint8_t* b_scales, int64_t M, int64_t N,
+                     int64_t K, const int32_t* row_offsets, int32_t n_groups,
+                     const int32_t* row_index, void* out, int32_t out_dtype, int64_t ld_out,
+                     void* stream);
+
+/*
+ * moe_mxfp4_matmul_kgroup -- products over ranges of the contraction, the
+ * weight gradients of the experts: out[g] [M][N] = A[:, range g] B[:, range
+ * g]^T.
+ *   a_codes  [M][K/2], a_scales [M][K/32]; b_codes [N][K/2], b_scales [N][K/32]
+ *            (codes_t and scales_t of moe_mxfp4_pack, K its padded rows)
+ *   k_offsets [n_groups + 1] i32, non-decreasing multiples of 32 (its
+ *            padded_offsets), or NULL (n_groups = 1: all of K).  An empty range
+ *            gives zeros
+ *   out      [n_groups][M][N] of out_dtype
+ */
+int moe_mxfp4_matmul_kgroup(const uint8_t* a_codes, const uint8_t* a_scales,
+                            const uint8_t* b_codes, const uint8_t* b_scales, int64_t M, int64_t N,
+                            int64_t K, const int32_t* k_offsets, int32_t n_groups, void* out,
+                            int32_t out_dtype, void* stream);
+
+/*
+ * moe_mxfp4_linear -- moe_mxfp4_matmul of activations that are packed on the
+ * way: x [x_rows][K] of x_dtype (MOE_F32, MOE_BF16, MOE_F16), rows row_stride
+ * elements apart, against packed weights [n_groups][N].  The same bits as
+ * moe_mxfp4_pack followed by moe_mxfp4_matmul, up to the order of the sums over
+ * K.  A few rows (a token being decoded) are packed in registers, in one launch.
+ *   workspace: >= moe_mxfp4_linear_workspace_bytes(x_rows, K) bytes, 256-byte
+ *            aligned
+ */
+size_t moe_mxfp4_linear_workspace_bytes(int64_t x_rows, int64_t K);
+
+int moe_mxfp4_linear(const void* x, int32_t x_dtype, int64_t x_rows, int64_t row_stride,
+                     const uint8_t* w_codes, const uint8_t* w_scales, int64_t M, int64_t N,
+                     int64_t K, const int32_t* row_offsets, int32_t n_groups,
+                     const int32_t* row_index, void* out, int32_t out_dtype, int64_t ld_out,
+                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static description of a moe_status value; never NULL. */
 const char* moe_status_str(int status);

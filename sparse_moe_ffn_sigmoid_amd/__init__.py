@@ -22,6 +22,7 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 MOE_F32, MOE_BF16, MOE_MXFP4, MOE_MXFP4_A8, MOE_MXFP4_A4 = 0, 1, 2, 3, 4
+MOE_F16 = 5
 MOE_QB_FROZEN, MOE_QB_BATCH = 0, 1
 EXPORTED = ("moe_route_workspace_bytes", "moe_route_qb", "moe_route_sign",
             "moe_forward_workspace_bytes",
@@ -29,7 +30,11 @@ EXPORTED = ("moe_route_workspace_bytes", "moe_route_qb", "moe_route_sign",
             "moe_stage_name", "moe_mxfp8_quantize", "moe_mxfp4_quantize",
             "moe_route_qb_noalloc", "moe_backward_workspace_bytes", "moe_latent_backward",
             "moe_sgd_step", "moe_latent_backward_sgd", "moe_saved_activations_bytes",
-            "moe_latent_forward_train", "moe_latent_backward_train")
+            "moe_latent_forward_train", "moe_latent_backward_train",
+            "moe_balance_loss_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward",
+            "moe_router_backward_workspace_bytes", "moe_router_backward",
+            "moe_mxfp4_padded_rows", "moe_mxfp4_pack", "moe_mxfp4_unpack", "moe_mxfp4_matmul",
+            "moe_mxfp4_matmul_kgroup", "moe_mxfp4_linear_workspace_bytes", "moe_mxfp4_linear")
 
 
 class MoeShape(ctypes.Structure):
@@ -105,6 +110,29 @@ _lib.moe_mxfp4_quantize.argtypes = [_vp, ctypes.c_int64, ctypes.c_int64, _vp, _v
 _lib.moe_mxfp4_quantize.restype = ctypes.c_int
 _lib.moe_mxfp8_quantize.argtypes = [_vp, ctypes.c_int64, ctypes.c_int64, _vp, _vp, _vp]
 _lib.moe_mxfp8_quantize.restype = ctypes.c_int
+_i64 = ctypes.c_int64
+for _name, _res, _args in (
+        ("moe_balance_loss_workspace_bytes", _sz, [_i32, _i32]),
+        ("moe_balance_loss", ctypes.c_int, [_vp, _i64, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp,
+                                            _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+        ("moe_balance_loss_backward", ctypes.c_int, [_vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp,
+                                                     _i32, _vp, _vp, _vp, _vp]),
+        ("moe_router_backward_workspace_bytes", _sz, [_i32, _i32, _i32]),
+        ("moe_router_backward", ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, ctypes.c_int,
+                                               _vp, _vp, _vp, _vp, _sz, _vp]),
+        ("moe_mxfp4_padded_rows", _i64, [_i64, _i32]),
+        ("moe_mxfp4_pack", ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp,
+                                          _vp, _vp, _i32, _vp, _vp]),
+        ("moe_mxfp4_unpack", ctypes.c_int, [_vp, _vp, _i64, _i64, _i32, _vp, _i64, _vp]),
+        ("moe_mxfp4_matmul", ctypes.c_int, [_vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i32,
+                                            _vp, _vp, _i32, _i64, _vp]),
+        ("moe_mxfp4_matmul_kgroup", ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i32,
+                                                   _vp, _i32, _vp]),
+        ("moe_mxfp4_linear_workspace_bytes", _sz, [_i64, _i64]),
+        ("moe_mxfp4_linear", ctypes.c_int, [_vp, _i32, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _vp,
+                                            _i32, _vp, _vp, _i32, _i64, _vp, _sz, _vp])):
+    getattr(_lib, _name).argtypes = _args
+    getattr(_lib, _name).restype = _res
 
 
 class MoeError(RuntimeError):
@@ -241,6 +269,333 @@ def mxfp4_quantize(x: torch.Tensor):
     return codes, scales
 
 
+# --------------------------------------------------------------------------
+# Balance loss and the dense gradient of the router's scores
+# --------------------------------------------------------------------------
+def _device_of(t, name):
+    """The GPU that a call runs on: that of its first tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU, got {t.device}")
+    return t.device
+
+
+def _call(fn, dev, *args):
+    """fn(*args, stream) on the device's current stream; raises MoeError."""
+    stream = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != 0:
+        raise MoeError(st, fn.__name__)
+
+
+def _workspace(workspace, need, dev):
+    if workspace is None:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    _check(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    return workspace
+
+
+def _score_rows(scores, name="scores"):
+    """Device, T, n and row stride of fp32 scores [T, n] with unit column stride."""
+    dev = _device_of(scores, name)
+    if scores.dim() != 2 or scores.dtype != torch.float32:
+        raise ValueError(f"{name} must be fp32 [T, n], got {scores.dtype} {tuple(scores.shape)}")
+    T, n = scores.shape
+    if n > 1 and scores.stride(1) != 1 or T > 1 and scores.stride(0) < n:
+        raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
+    return dev, T, n, (scores.stride(0) if T > 1 else n)
+
+
+def _sequences(seq_offsets, token_mask, dloss, T, dev):
+    """(number of sequences, mask as uint8), the arguments checked."""
+    S = 1
+    if seq_offsets is not None:
+        S = seq_offsets.numel() - 1
+        _check(seq_offsets, "seq_offsets", torch.int32, (S + 1,), dev)
+    if token_mask is not None:
+        if token_mask.dtype == torch.bool:
+            token_mask = token_mask.view(torch.uint8)
+        _check(token_mask, "token_mask", torch.uint8, (T,), dev)
+    if dloss is not None:
+        _check(dloss, "dloss", torch.float32, (S,), dev)
+    return S, token_mask
+
+
+def balance_loss(scores: torch.Tensor, idx: torch.Tensor, seq_offsets=None, token_mask=None,
+                 dloss=None, want_grad: bool = False, workspace=None):
+    """Balance loss of the routing idx [T, k] (int32; an index outside [0, n),
+    such as -1, is not counted) per sequence, with per-expert counts.
+
+    ``scores`` fp32 [T, n] >= 0 (rows may be strided); ``seq_offsets`` int32
+    [S + 1] (device) or None for one sequence; ``token_mask`` bool or uint8
+    [T], false for padding.  Over the N counted tokens of a sequence
+    loss = n / (k N^2) sum_i c_i sum_t s_ti / sum_j s_tj, 1 for even counts.
+    Returns dict(loss [S] fp32, counts [S, n] int32, tokens [S] int32), and
+    with ``want_grad`` dscores [T, n] fp32, the gradient of sum(loss * dloss)
+    (``dloss`` fp32 [S], None for ones) with the choices held fixed, from the
+    same pass over the scores.
+    """
+    dev, T, n, ld = _score_rows(scores)
+    if not isinstance(idx, torch.Tensor) or idx.dim() != 2:
+        raise ValueError("idx must be a tensor [T, k]")
+    k = idx.shape[1]
+    _check(idx, "idx", torch.int32, (T, k), dev)
+    S, mask = _sequences(seq_offsets, token_mask, dloss, T, dev)
+    out = dict(loss=torch.empty(S, dtype=torch.float32, device=dev),
+               counts=torch.empty((S, n), dtype=torch.int32, device=dev),
+               tokens=torch.empty(S, dtype=torch.int32, device=dev))
+    if want_grad:
+        out["dscores"] = torch.empty((T, n), dtype=torch.float32, device=dev)
+    ws = _workspace(workspace, _lib.moe_balance_loss_workspace_bytes(T, S), dev)
+    _call(_lib.moe_balance_loss, dev, _ptr(scores), ld, T, n, k, _ptr(idx), _ptr(seq_offsets), S,
+          _ptr(mask), _ptr(dloss), _ptr(out["loss"]), _ptr(out["counts"]), _ptr(out["tokens"]),
+          _ptr(out.get("dscores")), _ptr(ws), ws.numel())
+    return out
+
+
+def balance_loss_backward(scores: torch.Tensor, counts: torch.Tensor, tokens: torch.Tensor, k: int,
+                          seq_offsets=None, token_mask=None, dloss=None):
+    """dscores [T, n] of :func:`balance_loss` from the counts and tokens it
+    returned; the other arguments as it took them."""
+    dev, T, n, ld = _score_rows(scores)
+    S, mask = _sequences(seq_offsets, token_mask, dloss, T, dev)
+    _check(counts, "counts", torch.int32, (S, n), dev)
+    _check(tokens, "tokens", torch.int32, (S,), dev)
+    dscores = torch.empty((T, n), dtype=torch.float32, device=dev)
+    _call(_lib.moe_balance_loss_backward, dev, _ptr(scores), ld, T, n, k, _ptr(counts),
+          _ptr(tokens), _ptr(seq_offsets), S, _ptr(mask), _ptr(dloss), _ptr(dscores))
+    return dscores
+
+
+def router_backward(x: torch.Tensor, w_router: torch.Tensor, scores: torch.Tensor,
+                    dscores: torch.Tensor, into: dict | None = None, workspace=None):
+    """A gradient of all router scores (such as the balance loss's dscores)
+    taken to x [T, d] bf16, w_router [n, d] fp32 and the logit offset, for
+    scores = sigmoid(x w_router^T + offset) [T, n] fp32.
+
+    Returns dict(dx bf16, d_w_router fp32, d_router_logit_offset fp32).  With
+    ``into`` (a dict of :func:`latent_backward`) the gradients are added to
+    the tensors it holds under those names (entries that are None are left
+    out) and it is returned.
+    """
+    dev = _device_of(x, "x")
+    T, d = x.shape
+    n = w_router.shape[0]
+    _check(x, "x", torch.bfloat16, (T, d), dev)
+    _check(w_router, "w_router", torch.float32, (n, d), dev)
+    _check(scores, "scores", torch.float32, (T, n), dev)
+    _check(dscores, "dscores", torch.float32, (T, n), dev)
+    names = dict(dx=(torch.bfloat16, (T, d)), d_w_router=(torch.float32, (n, d)),
+                 d_router_logit_offset=(torch.float32, (n,)))
+    out = into
+    if into is None:
+        out = {f: torch.empty(shape, dtype=dt, device=dev) for f, (dt, shape) in names.items()}
+    else:
+        for f, (dt, shape) in names.items():
+            if into.get(f) is not None:
+                _check(into[f], f, dt, shape, dev)
+    need = _lib.moe_router_backward_workspace_bytes(T, d, n)
+    ws = _workspace(workspace, need, dev)
+    _call(_lib.moe_router_backward, dev, _ptr(x), _ptr(w_router), _ptr(scores), _ptr(dscores), T,
+          d, n, 0 if into is None else 1, *[_ptr(out.get(f)) for f in names], _ptr(ws),
+          ws.numel())
+    return out
+
+
+# --------------------------------------------------------------------------
+# MXFP4 packing and products
+# --------------------------------------------------------------------------
+_MX_TYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
+
+
+def _mx_type(dtype, name):
+    if dtype not in _MX_TYPES:
+        raise ValueError(f"{name} must be fp32, bf16 or fp16, got {dtype}")
+    return _MX_TYPES[dtype]
+
+
+def _mx_operand(codes, scales, name, dim, dev):
+    """Shape [.., rows, K] of packed codes [.., rows, K/2] and their scales."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != dim:
+        raise ValueError(f"{name}_codes must be a tensor of {dim} dimensions")
+    shape = tuple(codes.shape)
+    if shape[-1] == 0 or shape[-1] % 16:
+        raise ValueError(f"{name}_codes must hold whole blocks of 32 elements (16 bytes)")
+    _check(codes, f"{name}_codes", torch.uint8, shape, dev)
+    _check(scales, f"{name}_scales", torch.uint8, shape[:-1] + (shape[-1] // 16,), dev)
+    return shape[:-1] + (2 * shape[-1],)
+
+
+def mxfp4_pack(x: torch.Tensor, rows: bool = True, cols: bool = False, offsets=None):
+    """MXFP4 rounding of x [rows, K] or [batch, rows, K] (fp32, bf16 or fp16,
+    unit column stride) along rows and/or columns, from one read.
+
+    Returns a dict: with ``rows`` codes uint8 [.., rows, 16 ceil(K/32)] and
+    scales uint8 [.., rows, ceil(K/32)]; with ``cols`` codes_t uint8 [.., K,
+    16 R] and scales_t uint8 [.., K, R], R = ceil(rows/32).  Tails are filled
+    up with zeros.  With ``offsets`` int32 [G + 1] (2-D x, ``cols``) no block
+    of a column crosses from one row group to the next, each group starts at a
+    multiple of 32 padded rows, offsets_t int32 [G + 1], and R covers
+    rows + 31 G; rows outside every group are not touched.  A block with an
+    infinity or NaN becomes NaN.
+    """
+    dev = _device_of(x, "x")
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x must be [rows, K] or [batch, rows, K], got {tuple(x.shape)}")
+    dt = _mx_type(x.dtype, "x")
+    B = x.shape[0] if x.dim() == 3 else 1
+    R, K = x.shape[-2:]
+    rs = x.stride(-2) if R > 1 else max(K, 1)
+    bs = x.stride(0) if x.dim() == 3 and B > 1 else R * rs
+    if K < 1 or (K > 1 and x.stride(-1) != 1) or rs < K:
+        raise ValueError("x must have at least one column, unit column stride and rows that do "
+                         "not overlap")
+    if not rows and not cols:
+        raise ValueError("mxfp4_pack: neither rows nor cols asked for")
+    G = 0
+    if offsets is not None:
+        if not cols or x.dim() != 2:
+            raise ValueError("offsets need a matrix and cols=True")
+        G = offsets.numel() - 1
+        _check(offsets, "offsets", torch.int32, (G + 1,), dev)
+    lead = tuple(x.shape[:-2])
+    cb = (K + 31) // 32
+    out = {}
+    if rows:
+        out["codes"] = torch.empty(lead + (R, cb * 16), dtype=torch.uint8, device=dev)
+        out["scales"] = torch.empty(lead + (R, cb), dtype=torch.uint8, device=dev)
+    if cols:
+        padded = _lib.moe_mxfp4_padded_rows(R, G)
+        if padded < 0:
+            raise MoeError(-2, "moe_mxfp4_padded_rows")
+        out["codes_t"] = torch.empty(lead + (K, padded // 2), dtype=torch.uint8, device=dev)
+        out["scales_t"] = torch.empty(lead + (K, padded // 32), dtype=torch.uint8, device=dev)
+    if offsets is not None:
+        out["offsets_t"] = torch.empty(G + 1, dtype=torch.int32, device=dev)
+    _call(_lib.moe_mxfp4_pack, dev, _ptr(x), dt, B, R, K, rs, bs,
+          *[_ptr(out.get(f)) for f in ("codes", "scales", "codes_t", "scales_t")], _ptr(offsets),
+          G, _ptr(out.get("offsets_t")))
+    return out
+
+
+def mxfp4_unpack(codes: torch.Tensor, scales: torch.Tensor, K: int, dtype=torch.bfloat16):
+    """Values [.., rows, K] of packed rows (codes [.., rows, 16 ceil(K/32)]);
+    bf16 and fp32 hold them exactly, fp16 rounds them."""
+    dev = _device_of(codes, "codes")
+    dt = _mx_type(dtype, "dtype")
+    shape = _mx_operand(codes, scales, "", codes.dim(), dev)
+    if len(shape) < 2 or not shape[-1] - 32 < K <= shape[-1]:
+        raise ValueError(f"K = {K} does not fit codes of {shape[-1]} elements")
+    out = torch.empty(shape[:-1] + (K,), dtype=dtype, device=dev)
+    _call(_lib.moe_mxfp4_unpack, dev, _ptr(codes), _ptr(scales), out.numel() // K, K, dt,
+          _ptr(out), K)
+    return out
+
+
+def _groups(offsets, b_dim, dev):
+    if offsets is None:
+        if b_dim != 2:
+            raise ValueError("a matrix per group needs offsets")
+        return 1
+    _check(offsets, "offsets", torch.int32, (offsets.numel(),), dev)
+    return offsets.numel() - 1
+
+
+def _mx_out(out, M, N, dtype, dev):
+    """The output [M, N] and its row stride: given (rows may be strided) or new."""
+    if out is None:
+        return torch.empty((M, N), dtype=dtype, device=dev), N
+    if out.device != dev or out.dtype != dtype or tuple(out.shape) != (M, N):
+        raise ValueError(f"out must be {dtype} {(M, N)} on {dev}")
+    if (N > 1 and out.stride(1) != 1) or (M > 1 and out.stride(0) < N):
+        raise ValueError("out must have unit column stride and rows that do not overlap")
+    return out, out.stride(0) if M > 1 else N
+
+
+def mxfp4_matmul(a_codes, a_scales, b_codes, b_scales, offsets=None, rows=None,
+                 out_dtype=torch.bfloat16, out=None):
+    """C [M, N] = A B^T of MXFP4 operands A [R, K] and B [N, K], packed along K.
+
+    With ``offsets`` int32 [G + 1] (device) and B [G, N, K] rows [offsets[g],
+    offsets[g + 1]) of C meet B[g]; rows outside every group stay as they were
+    (undefined unless ``out`` is given).  ``rows`` int32 [M] (device): row r of
+    C is made from row rows[r] of A, M = R without it.
+    """
+    dev = _device_of(a_codes, "a_codes")
+    R, K = _mx_operand(a_codes, a_scales, "a", 2, dev)
+    G = _groups(offsets, b_codes.dim(), dev)
+    b = _mx_operand(b_codes, b_scales, "b", 2 if offsets is None else 3, dev)
+    if b[-1] != K or (offsets is not None and b[0] != G):
+        raise ValueError(f"b is {b}: K = {K} and {G} groups are wanted")
+    M, N = R, b[-2]
+    if rows is not None:
+        M = rows.numel()
+        _check(rows, "rows", torch.int32, (M,), dev)
+    dt = _mx_type(out_dtype, "out_dtype")
+    out, ldo = _mx_out(out, M, N, out_dtype, dev)
+    _call(_lib.moe_mxfp4_matmul, dev, _ptr(a_codes), _ptr(a_scales), R, _ptr(b_codes),
+          _ptr(b_scales), M, N, K, _ptr(offsets), G, _ptr(rows), _ptr(out), dt, ldo)
+    return out
+
+
+def mxfp4_matmul_kgroup(a_codes, a_scales, b_codes, b_scales, offsets=None,
+                        out_dtype=torch.float32):
+    """Products over ranges of the contraction, the weight gradients of a
+    linear layer or of experts: out[g] = A[:, range g] B[:, range g]^T of
+    A [M, K] and B [N, K] (codes_t and scales_t of :func:`mxfp4_pack`), ranges
+    from ``offsets`` (its offsets_t).  Returns [G, M, N], or [M, N] over all of
+    K without ``offsets``."""
+    dev = _device_of(a_codes, "a_codes")
+    M, K = _mx_operand(a_codes, a_scales, "a", 2, dev)
+    N, Kb = _mx_operand(b_codes, b_scales, "b", 2, dev)
+    if Kb != K:
+        raise ValueError(f"the operands' K differ: {K} and {Kb}")
+    dt = _mx_type(out_dtype, "out_dtype")
+    G = 1
+    if offsets is not None:
+        G = offsets.numel() - 1
+        _check(offsets, "offsets", torch.int32, (G + 1,), dev)
+    out = torch.empty(((G,) if offsets is not None else ()) + (M, N), dtype=out_dtype, device=dev)
+    _call(_lib.moe_mxfp4_matmul_kgroup, dev, _ptr(a_codes), _ptr(a_scales), _ptr(b_codes),
+          _ptr(b_scales), M, N, K, _ptr(offsets), G, _ptr(out), dt)
+    return out
+
+
+def mxfp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, offsets=None,
+                 rows=None, out_dtype=None, out=None, workspace=None):
+    """:func:`mxfp4_matmul` of activations x [R, K] (fp32, bf16 or fp16, K a
+    multiple of 32) that are packed on the way, against packed weights [N, K],
+    or [G, N, K] with ``offsets``.  ``out_dtype`` defaults to x's."""
+    dev = _device_of(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [R, K], got {tuple(x.shape)}")
+    xt = _mx_type(x.dtype, "x")
+    R, K = x.shape
+    rs = x.stride(0) if R > 1 else K
+    if x.stride(1) != 1 and K > 1 or rs < K:
+        raise ValueError("x must have unit column stride and rows that do not overlap")
+    G = _groups(offsets, w_codes.dim(), dev)
+    w = _mx_operand(w_codes, w_scales, "w", 2 if offsets is None else 3, dev)
+    if w[-1] != K or (offsets is not None and w[0] != G):
+        raise ValueError(f"the weights are {w}: K = {K} and {G} groups are wanted")
+    M, N = R, w[-2]
+    if rows is not None:
+        M = rows.numel()
+        _check(rows, "rows", torch.int32, (M,), dev)
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    dt = _mx_type(out_dtype, "out_dtype")
+    out, ldo = _mx_out(out, M, N, out_dtype, dev)
+    ws = _workspace(workspace, _lib.moe_mxfp4_linear_workspace_bytes(R, K), dev)
+    _call(_lib.moe_mxfp4_linear, dev, _ptr(x), xt, R, rs, _ptr(w_codes), _ptr(w_scales), M, N, K,
+          _ptr(offsets), G, _ptr(rows), _ptr(out), dt, ldo, _ptr(ws), ws.numel())
+    return out
+
+
 GRAD_SHAPES = {  # gradient name -> (weight key, shape from (T, d, L, n, k, m, ms))
     "d_w_router": ("w_router", lambda T, d, L, n, k, m, ms: (n, d)),
     "d_router_logit_offset": ("router_logit_offset", lambda T, d, L, n, k, m, ms: (n,)),
@@ -257,11 +612,14 @@ GRAD_SHAPES = {  # gradient name -> (weight key, shape from (T, d, L, n, k, m, m
 
 
 def latent_backward(shape: MoeShape, weights: dict, x: torch.Tensor, scores: torch.Tensor,
-                    idx: torch.Tensor, w: torch.Tensor, dout: torch.Tensor, workspace=None):
+                    idx: torch.Tensor, w: torch.Tensor, dout: torch.Tensor, workspace=None,
+                    dscores=None):
     """Gradients of sum(out * dout) for a forward call with routing (scores
     [T,n] f32, idx [T,k] i32, w [T,k] f32), the selection held fixed.  Returns
     dict(dx, d_w_router, ...): fp32 weight gradients, dx in the activation
-    dtype (bf16 layers only)."""
+    dtype (bf16 layers only).  ``dscores`` [T,n] f32: a further gradient of
+    the scores, such as the balance loss's, that :func:`router_backward` adds
+    to dx, d_w_router and d_router_logit_offset."""
     dev = x.device
     T, d, l, n, k = shape.T, shape.d, shape.latent, shape.n_experts, shape.top_k
     m, ms = shape.inter, shape.shared_inter
@@ -288,6 +646,8 @@ def latent_backward(shape: MoeShape, weights: dict, x: torch.Tensor, scores: tor
                                   ws.numel(), _stream())
     if st != 0:
         raise MoeError(st, "moe_latent_backward")
+    if dscores is not None:
+        router_backward(x, weights["w_router"], scores, dscores, into=out)
     return out
 
 
@@ -333,11 +693,14 @@ def latent_backward_sgd(shape: MoeShape, weights: dict, x: torch.Tensor, scores:
 
 def latent_backward_train(shape: MoeShape, weights: dict, x: torch.Tensor, scores: torch.Tensor,
                           idx: torch.Tensor, w: torch.Tensor, dout: torch.Tensor,
-                          saved: torch.Tensor, lr=None, workspace=None):
+                          saved: torch.Tensor, lr=None, workspace=None, dscores=None):
     """The backward of a training forward (latent_forward with `saved`),
     reading the activations it kept.  lr None: every gradient, as
     latent_backward; else the SGD step is applied as in latent_backward_sgd
-    (the experts' gradients in place, not returned)."""
+    (the experts' gradients in place, not returned).  ``dscores`` as for
+    latent_backward; not with lr, whose step comes before it could be added."""
+    if dscores is not None and lr is not None:
+        raise ValueError("dscores needs lr=None (apply sgd_step to the gradients)")
     dev = x.device
     T, d, l, n, k = shape.T, shape.d, shape.latent, shape.n_experts, shape.top_k
     m, ms = shape.inter, shape.shared_inter
@@ -368,6 +731,8 @@ def latent_backward_train(shape: MoeShape, weights: dict, x: torch.Tensor, score
                                         ws.numel(), _stream())
     if st != 0:
         raise MoeError(st, "moe_latent_backward_train")
+    if dscores is not None:
+        router_backward(x, weights["w_router"], scores, dscores, into=out)
     return out
 
 

@@ -1,0 +1,278 @@
+// A gradient of all the router's scores taken to the tokens, the router's
+// weights and its logit offset: with g = dscores s (1 - s) for sigmoid scores,
+//
+//   dx = g W_r  [T][d],   dW_r = g^T x  [n][d],   d_offset = sum_t g  [n]
+//
+// Two products of 2 T n d operations each on the bf16 MFMA.  Their operands
+// are written K-contiguous once by the kernels here (g both ways, W_r and x
+// transposed), a few per cent of the products' time.  dW_r is an fp32 output:
+// g enters it as the exact sum of three bf16 parts (24 bits), three segments of
+// one contraction against the same bf16 x.  dx is rounded to bf16: two parts of
+// g and of W_r (16 bits each) are kept, without the product of the low parts.
+#include <algorithm>
+
+#include "common.hpp"
+#include "gemm.hpp"
+#include "layer_kernels.hpp"
+
+namespace moe {
+namespace router {
+
+constexpr int TILE = 64;
+
+// What bf16 rounding left of v, rounded in turn.
+__device__ __forceinline__ void split2(float v, bf16_t& hi, bf16_t& lo) {
+  hi = f32_to_bf16(v);
+  lo = f32_to_bf16(v - bf16_to_f32(hi));
+}
+
+// Eight values to one 16-byte store.
+__device__ __forceinline__ void store8(bf16_t* p, const bf16_t (&v)[8]) {
+  uint4 q;
+  q.x = v[0] | (static_cast<uint32_t>(v[1]) << 16);
+  q.y = v[2] | (static_cast<uint32_t>(v[3]) << 16);
+  q.z = v[4] | (static_cast<uint32_t>(v[5]) << 16);
+  q.w = v[6] | (static_cast<uint32_t>(v[7]) << 16);
+  *reinterpret_cast<uint4*>(p) = q;
+}
+
+// g of 64 tokens x 64 experts: by token [T][np] in two parts, by expert [n][Tp]
+// in three, zeros behind the ends, and the tile's sum per expert.
+__global__ __launch_bounds__(256) void score_grad_k(const float* __restrict__ scores,
+                                                    const float* __restrict__ dscores, int T,
+                                                    int n, int64_t np, int64_t Tp,
+                                                    bf16_t* __restrict__ g_hi,
+                                                    bf16_t* __restrict__ g_lo,
+                                                    bf16_t* __restrict__ gt_hi,
+                                                    bf16_t* __restrict__ gt_mid,
+                                                    bf16_t* __restrict__ gt_lo,
+                                                    float* __restrict__ part) {
+  __shared__ float tile[TILE][TILE + 1];
+  const int e0 = blockIdx.x * TILE, t0 = blockIdx.y * TILE;
+  for (int i = threadIdx.x; i < TILE * TILE; i += 256) {
+    const int t = i / TILE, e = i % TILE;
+    float g = 0.f;
+    if (t0 + t < T && e0 + e < n) {
+      const int64_t at = static_cast<int64_t>(t0 + t) * n + e0 + e;
+      const float s = scores[at];
+      g = dscores[at] * (s * (1.f - s));
+    }
+    tile[t][e] = g;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < TILE * TILE / 8; i += 256) {
+    const int r = i / 8, c = i % 8 * 8;
+    bf16_t hi[8], mid[8], lo[8];
+    if (t0 + r < T) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) split2(tile[r][c + j], hi[j], lo[j]);
+      const int64_t at = static_cast<int64_t>(t0 + r) * np + e0 + c;
+      store8(g_hi + at, hi);
+      store8(g_lo + at, lo);
+    }
+    if (e0 + r < n) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = tile[c + j][r];
+        split2(v, hi[j], mid[j]);
+        lo[j] = f32_to_bf16((v - bf16_to_f32(hi[j])) - bf16_to_f32(mid[j]));
+      }
+      const int64_t at = (e0 + r) * Tp + t0 + c;
+      store8(gt_hi + at, hi);
+      store8(gt_mid + at, mid);
+      store8(gt_lo + at, lo);
+    }
+  }
+  if (threadIdx.x < TILE) {
+    float sum = 0.f;
+#pragma unroll 8
+    for (int t = 0; t < TILE; ++t) sum += tile[t][threadIdx.x];
+    part[blockIdx.y * np + e0 + threadIdx.x] = sum;
+  }
+}
+
+// out[c][r] = in[r][c], zeros from R to ld_out; fp32 input in two parts.
+template <typename IN>
+__global__ __launch_bounds__(256) void transpose_k(const IN* __restrict__ in, int R, int C,
+                                                   int64_t ld_out, bf16_t* __restrict__ hi,
+                                                   bf16_t* __restrict__ lo) {
+  __shared__ IN tile[TILE][TILE + 1];
+  const int c0 = blockIdx.x * TILE, r0 = blockIdx.y * TILE;
+  for (int i = threadIdx.x; i < TILE * TILE; i += 256) {
+    const int r = i / TILE, c = i % TILE;
+    tile[r][c] = r0 + r < R ? in[static_cast<int64_t>(r0 + r) * C + c0 + c] : IN(0);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < TILE * TILE / 8; i += 256) {
+    const int c = i / 8, r = i % 8 * 8;
+    const int64_t at = (c0 + c) * ld_out + r0 + r;
+    bf16_t h[8], l[8];
+    if constexpr (std::is_same<IN, float>::value) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) split2(tile[r + j][c], h[j], l[j]);
+      store8(lo + at, l);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = tile[r + j][c];
+    }
+    store8(hi + at, h);
+  }
+}
+
+// d_offset from the tiles' sums, in 64 bits and a fixed order
+__global__ __launch_bounds__(256) void offset_k(const float* __restrict__ part, int tiles, int n,
+                                                int64_t np, int accumulate,
+                                                float* __restrict__ out) {
+  __shared__ double red[4][64];
+  const int e = blockIdx.x * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6;
+  double sum = 0.0;
+  if (e < n)
+    for (int t = w; t < tiles; t += 4) sum += part[t * np + e];
+  red[w][threadIdx.x & 63] = sum;
+  __syncthreads();
+  if (w == 0 && e < n) {
+    sum = red[0][threadIdx.x] + red[1][threadIdx.x] + red[2][threadIdx.x] + red[3][threadIdx.x];
+    out[e] = accumulate ? out[e] + static_cast<float>(sum) : static_cast<float>(sum);
+  }
+}
+
+template <typename OUT>
+__global__ __launch_bounds__(256) void add_k(const float* __restrict__ v, int64_t count,
+                                             OUT* __restrict__ out) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < count;
+       i += static_cast<int64_t>(gridDim.x) * 256)
+    out[i] = from_f32<OUT>(to_f32<OUT>(out[i]) + v[i]);
+}
+
+struct Workspace {
+  bf16_t *g_hi, *g_lo, *gt_hi, *gt_mid, *gt_lo, *wt_hi, *wt_lo, *xt;
+  float *part, *sum, *partial;
+  size_t partial_bytes;
+};
+
+static int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
+
+static size_t layout(int T, int d, int n, Workspace* out, void* base) {
+  Carver cv(base);
+  Workspace w{};
+  const int64_t np = up64(n), Tp = up64(T);
+  w.g_hi = cv.take<bf16_t>(T * np);
+  w.g_lo = cv.take<bf16_t>(T * np);
+  w.gt_hi = cv.take<bf16_t>(n * Tp);
+  w.gt_mid = cv.take<bf16_t>(n * Tp);
+  w.gt_lo = cv.take<bf16_t>(n * Tp);
+  w.wt_hi = cv.take<bf16_t>(d * np);
+  w.wt_lo = cv.take<bf16_t>(d * np);
+  w.xt = cv.take<bf16_t>(d * Tp);
+  w.part = cv.take<float>(Tp / 64 * np);
+  w.sum = cv.take<float>(static_cast<int64_t>(std::max(T, n)) * d);
+  w.partial_bytes =
+      std::max({gemm::splitk_bytes(T, d, static_cast<int>(3 * np), gemm::EPI_BF16),
+                gemm::splitk_bytes(T, d, static_cast<int>(3 * np), gemm::EPI_F32),
+                gemm::splitk_bytes(n, d, static_cast<int>(3 * Tp), gemm::EPI_F32)});
+  w.partial = cv.take<float>(w.partial_bytes / 4);
+  if (out) *out = w;
+  return cv.bytes();
+}
+
+static int check(int32_t T, int32_t d, int32_t n) {
+  if (T < 0 || d <= 0 || d % 64 || n < 1) return MOE_EINVAL;
+  if (n > 1024 || T > MOE_MAX_TOKENS || d > (1 << 20)) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+static unsigned grid_of(int64_t count) {
+  return static_cast<unsigned>(std::min<int64_t>((count + 255) / 256, 8192));
+}
+
+// C = sum of three products A_i B_i^T over one contraction each of K
+static int product3(const Workspace& w, const bf16_t* const (&A)[3], const bf16_t* const (&B)[3],
+                    int64_t K, int M, int N, void* C, int epi, hipStream_t st) {
+  gemm::Params p{};
+  p.M = M;
+  p.N = N;
+  p.nseg = 3;
+  for (int i = 0; i < 3; ++i) p.seg[i] = layer::seg(A[i], K, B[i], K, static_cast<int>(K));
+  p.C = C;
+  p.ldc = N;
+  p.partial = w.partial_bytes ? w.partial : nullptr;
+  p.partial_bytes = w.partial_bytes;
+  return gemm::launch(p, epi, gemm::B_DENSE, true, 128, st);
+}
+
+}  // namespace router
+}  // namespace moe
+
+extern "C" size_t moe_router_backward_workspace_bytes(int32_t T, int32_t d, int32_t n) {
+  if (moe::router::check(T, d, n) != MOE_OK) return 0;
+  return std::max<size_t>(moe::router::layout(T, d, n, nullptr, nullptr), 256);
+}
+
+extern "C" int moe_router_backward(const void* x, const float* w_router, const float* scores,
+                                   const float* dscores, int32_t T, int32_t d, int32_t n,
+                                   int accumulate, void* dx, float* d_w_router,
+                                   float* d_router_logit_offset, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  using namespace moe;
+  using namespace moe::router;
+  int rc = check(T, d, n);
+  if (rc != MOE_OK) return rc;
+  if (T > 0 && (!scores || !dscores || (dx && !w_router) || (d_w_router && !x)))
+    return MOE_EINVAL;
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MOE_EINVAL;
+  if (reinterpret_cast<uintptr_t>(dx) % 16 != 0 || reinterpret_cast<uintptr_t>(d_w_router) % 16 != 0)
+    return MOE_EINVAL;
+  Workspace w;
+  if (workspace_bytes < layout(T, d, n, &w, workspace)) return MOE_EWORKSPACE;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const int64_t np = up64(n), Tp = up64(T), nd = static_cast<int64_t>(n) * d;
+  if (T == 0) {
+    if (!accumulate && d_w_router)
+      hipLaunchKernelGGL(layer::fill_u32, dim3(grid_of(nd)), dim3(256), 0, st,
+                         reinterpret_cast<uint32_t*>(d_w_router), 0u, nd);
+    if (!accumulate && d_router_logit_offset)
+      hipLaunchKernelGGL(layer::fill_u32, dim3(grid_of(n)), dim3(256), 0, st,
+                         reinterpret_cast<uint32_t*>(d_router_logit_offset), 0u,
+                         static_cast<int64_t>(n));
+    MOE_LAUNCH_CHECK();
+    return MOE_OK;
+  }
+  const unsigned tn = static_cast<unsigned>(np / 64), tt = static_cast<unsigned>(Tp / 64),
+                 td = static_cast<unsigned>(d / 64);
+  hipLaunchKernelGGL(score_grad_k, dim3(tn, tt), dim3(256), 0, st, scores, dscores, T, n, np, Tp,
+                     w.g_hi, w.g_lo, w.gt_hi, w.gt_mid, w.gt_lo, w.part);
+  MOE_LAUNCH_CHECK();
+  if (d_router_logit_offset) {
+    hipLaunchKernelGGL(offset_k, dim3(tn), dim3(256), 0, st, w.part, static_cast<int>(tt), n, np,
+                       accumulate, d_router_logit_offset);
+    MOE_LAUNCH_CHECK();
+  }
+  if (d_w_router) {
+    hipLaunchKernelGGL(transpose_k<bf16_t>, dim3(td, tt), dim3(256), 0, st,
+                       static_cast<const bf16_t*>(x), T, d, Tp, w.xt, nullptr);
+    MOE_LAUNCH_CHECK();
+    rc = product3(w, {w.gt_hi, w.gt_mid, w.gt_lo}, {w.xt, w.xt, w.xt}, Tp, n, d,
+                  accumulate ? w.sum : d_w_router, gemm::EPI_F32, st);
+    if (rc != MOE_OK) return rc;
+    if (accumulate) {
+      hipLaunchKernelGGL(add_k<float>, dim3(grid_of(nd)), dim3(256), 0, st, w.sum, nd, d_w_router);
+      MOE_LAUNCH_CHECK();
+    }
+  }
+  if (dx) {
+    hipLaunchKernelGGL(transpose_k<float>, dim3(td, tn), dim3(256), 0, st, w_router, n, d, np,
+                       w.wt_hi, w.wt_lo);
+    MOE_LAUNCH_CHECK();
+    rc = product3(w, {w.g_hi, w.g_hi, w.g_lo}, {w.wt_hi, w.wt_lo, w.wt_hi}, np, T, d,
+                  accumulate ? static_cast<void*>(w.sum) : dx,
+                  accumulate ? gemm::EPI_F32 : gemm::EPI_BF16, st);
+    if (rc != MOE_OK) return rc;
+    if (accumulate) {
+      const int64_t count = static_cast<int64_t>(T) * d;
+      hipLaunchKernelGGL(add_k<bf16_t>, dim3(grid_of(count)), dim3(256), 0, st, w.sum, count,
+                         static_cast<bf16_t*>(dx));
+      MOE_LAUNCH_CHECK();
+    }
+  }
+  return MOE_OK;
+}
