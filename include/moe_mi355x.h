@@ -513,7 +513,7 @@ int moe_mxfp4_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, 
  *            row_offsets[g + 1]) of C meet matrix g.  Rows of C outside every
  *            group are left as they were
  *   row_index [M] i32 or NULL: row r of C is made from row row_index[r] of A
- *            (an index outside [0, a_rows) stands for a row of zeros); NULL: row r
+ *            (an index outside [0, a_rows) makes it a row of zeros); NULL: row r
  *   out      [M][N] of out_dtype (MOE_F32, MOE_BF16, MOE_F16), rows ld_out
  *            elements apart, rounded once from the fp32 sum
  */

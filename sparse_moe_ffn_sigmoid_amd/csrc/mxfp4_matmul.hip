@@ -25,6 +25,8 @@
 namespace moe {
 namespace mx {
 
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef int v4i_t __attribute__((ext_vector_type(4)));
 typedef int v8i_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
@@ -32,8 +34,7 @@ typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 constexpr int FP4 = 4;  // E2M1 in the scaled MFMA's format fields
 
-// What a chunk outside the operands reads as: codes of zero.
-__device__ __attribute__((aligned(16))) const uint8_t zero_chunk[16] = {};
+typedef const __attribute__((address_space(1))) uint8_t* global_ptr;
 
 struct MatArgs {
   const uint8_t *A, *As, *B, *Bs;
@@ -49,7 +50,13 @@ struct MatArgs {
   void* C;
   int64_t ldc, c_stride;       // elements; c_stride between K groups
   int out;                     // MOE_F32, MOE_BF16 or MOE_F16
+  int vec_out;                 // rows of C can be written 16 bytes at a time
 };
+
+// 32 codes as a matrix operand: E2M1 takes the first four registers, the rest is not read
+__device__ __forceinline__ v8i_t fp4_operand(v4i_t v) {
+  return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
+}
 
 __device__ __forceinline__ void store_one(const MatArgs& a, int64_t at, float v) {
   if (a.out == MOE_F32)
@@ -65,254 +72,479 @@ __device__ __forceinline__ int group_begin(const MatArgs& a, int g) {
   return min(max(a.off[g], 0), a.M);
 }
 
+// Whether row r of C comes from nowhere: its values are zeros.
+__device__ __forceinline__ bool absent(const MatArgs& a, int64_t r) {
+  if (!a.a_rows) return false;
+  const int at = a.a_rows[r];
+  return at < 0 || at >= a.a_count;
+}
+
 struct Tile {
   int g, row0, rows, n0;
   int kb0, kb1;  // blocks of 32 along K
 };
 
-// Group of row tile m.  Group g owns the indices from off[g] / BM + g on, one
-// per tile: the next group's first index is beyond them, because its rows start
-// no earlier than this group's end.  No list of tiles is built.
-template <int BM>
-__device__ __forceinline__ bool find_rows(const MatArgs& a, int m, Tile& t) {
-  if (!a.off) {
-    t.g = 0;
-    t.row0 = m * BM;
-    t.rows = min(BM, a.M - t.row0);
-    return t.rows > 0;
+// 16 scale bytes from block kb < kb1 of a row on.  Blocks at or behind kb1 read
+// as scale 2^-127 on both sides: whatever codes stand there, their products are
+// below 2^-240, nothing next to an fp32 sum.
+__device__ __forceinline__ uint4 scales16(global_ptr row, int kb, int kb1) {
+  if (kb + 16 <= kb1) {
+    struct __attribute__((packed, aligned(1))) Sixteen {
+      uint32_t x, y, z, w;
+    };
+    const auto* p = reinterpret_cast<const __attribute__((address_space(1))) Sixteen*>(row + kb);
+    return make_uint4(p->x, p->y, p->z, p->w);
   }
-  int lo = 0, hi = a.G;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (group_begin(a, mid) / BM + mid <= m)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  const int beg = group_begin(a, lo), end = group_begin(a, lo + 1);
-  const int64_t row = beg + (static_cast<int64_t>(m) - (beg / BM + lo)) * BM;
-  if (row < beg || row >= end) return false;
-  t.g = lo;
-  t.row0 = static_cast<int>(row);
-  t.rows = min(BM, end - t.row0);
-  return true;
+  uint32_t v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = row[min(kb + i, kb1 - 1)];
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (kb + i < kb1) w[i >> 2] |= v[i] << (8 * (i & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Block -> tile.  Blocks are dealt to the 8 XCDs in turn, so a block's number is
-// turned into one that runs through consecutive tiles on one XCD; row tiles
-// come fastest within GM of them, so that the tiles an XCD works on at one time
-// share their rows of A and B in its L2.
-template <int BM, int BN>
-__device__ __forceinline__ bool find_tile(const MatArgs& a, int ntm, int ntn, Tile& t) {
-  constexpr int GM = 4;
-  const int64_t G = gridDim.x, b = blockIdx.x;
-  int64_t tau = (b & 7) * (G >> 3) + (b >> 3);
-  const int64_t per = static_cast<int64_t>(ntm) * ntn;
-  int kg = 0;
-  if (a.kofs) {
-    if (tau >= per * a.G) return false;
-    kg = static_cast<int>(tau / per);
-    tau -= kg * per;
-  } else if (tau >= per) {
-    return false;
+// Four consecutive outputs of a row in the output's type.
+template <int OUT>
+struct Quad;
+template <>
+struct Quad<MOE_F32> {
+  typedef uint4 type;
+  static __device__ __forceinline__ uint4 make(float a, float b, float c, float d) {
+    return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c),
+                      __float_as_uint(d));
   }
-  const int64_t grp = tau / (GM * ntn);
-  const int gm = static_cast<int>(min(static_cast<int64_t>(GM), ntm - grp * GM));
-  const int64_t r = tau - grp * GM * ntn;
-  const int m = static_cast<int>(grp * GM + r % gm);
-  t.n0 = static_cast<int>(r / gm) * BN;
-  t.kb0 = 0;
-  t.kb1 = static_cast<int>(a.K / 32);
-  if (a.kofs) {
-    t.g = kg;
-    t.row0 = m * BM;
-    t.rows = min(BM, a.M - t.row0);
-    // inside the operands whatever the offsets hold
-    t.kb0 = static_cast<int>(min(max(static_cast<int64_t>(a.kofs[kg]), int64_t(0)), a.K) / 32);
-    t.kb1 = static_cast<int>(min(max(static_cast<int64_t>(a.kofs[kg + 1]), int64_t(0)), a.K) / 32);
-    return true;
-  }
-  return find_rows<BM>(a, m, t);
-}
-
-// 8 scale bytes from block kb of a row on; what lies at or behind kb1 reads as
-// 127 (one), which leaves zero codes zero.
-__device__ __forceinline__ uint2 scales8(const uint8_t* row, int kb, int kb1) {
-  uint2 v;
-  if (kb + 8 <= kb1) {
-    __builtin_memcpy(&v, row + kb, 8);
+};
+template <>
+struct Quad<MOE_BF16> {
+  typedef uint2 type;
+  static __device__ __forceinline__ uint2 make(float a, float b, float c, float d) {
+    const bf16x2_t lo = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+    const bf16x2_t hi = {static_cast<__bf16>(c), static_cast<__bf16>(d)};
+    uint2 v;
+    __builtin_memcpy(&v.x, &lo, 4);
+    __builtin_memcpy(&v.y, &hi, 4);
     return v;
   }
-  uint32_t w[2] = {0x7f7f7f7fu, 0x7f7f7f7fu};
-  for (int i = 0; kb + i < kb1; ++i)
-    w[i >> 2] = (w[i >> 2] & ~(255u << (8 * (i & 3)))) |
-                (static_cast<uint32_t>(row[kb + i]) << (8 * (i & 3)));
-  return make_uint2(w[0], w[1]);
-}
+};
+template <>
+struct Quad<MOE_F16> {
+  typedef uint2 type;
+  static __device__ __forceinline__ uint2 make(float a, float b, float c, float d) {
+    const f16x2_t lo = {static_cast<_Float16>(a), static_cast<_Float16>(b)};
+    const f16x2_t hi = {static_cast<_Float16>(c), static_cast<_Float16>(d)};
+    uint2 v;
+    __builtin_memcpy(&v.x, &lo, 4);
+    __builtin_memcpy(&v.y, &hi, 4);
+    return v;
+  }
+};
 
+// WM x WN waves, up to FM x FN fragments of 32 x 32 each.  Fragment i of wave
+// row wm covers tile rows (i WM + wm) 32 ..: a short tile's fragments are
+// spread evenly over the waves, and a tile of r rows runs the body for
+// NF = ceil(r / (32 WM)) fragments, free of branches.  The matrix instruction
+// gets the weights as its first operand, so that a lane holds four consecutive
+// columns of one output row.
+//
+// A block stays and takes one tile after another: the next tile's first copies
+// and scales are on their way while the finished one is written out.
 template <int WM, int WN, int FM, int FN>
-__global__ __launch_bounds__(64 * WM * WN) void ring_k(MatArgs a, int ntm, int ntn) {
-  constexpr int NW = WM * WN, NTH = 64 * NW;
-  constexpr int BM = WM * FM * 32, BN = WN * FN * 32;
-  constexpr int AI = BM / 8, BI = BN / 8;  // 1 KB copies of 8 rows per buffer
-  constexpr int MA = (AI + NW - 1) / NW, MB = (BI + NW - 1) / NW;
-  constexpr int MS = (BM + BN + NTH - 1) / NTH;  // scale rows per thread
-  __shared__ __attribute__((aligned(1024))) uint8_t sA[2][BM * 128];
-  __shared__ __attribute__((aligned(1024))) uint8_t sB[2][BN * 128];
-  __shared__ __attribute__((aligned(16))) uint2 sS[2][BM + BN];
+struct Ring {
+  static constexpr int NW = WM * WN, NTH = 64 * NW;
+  static constexpr int BM = WM * FM * 32, BN = WN * FN * 32;
+  // Copies into the buffers (1 KB, 8 rows) are made by half of the waves, one on
+  // each SIMD: a wave is held up until the address unit has taken its copies, and
+  // its neighbour has the matrix unit meanwhile.
+  static constexpr int LW = NW / 2;
+  static constexpr int MB = BN / 8 / LW;
+  static_assert(MB * 8 * LW == BN && (WM * 32) % (8 * LW) == 0, "whole copies per wave");
+  static constexpr int AC = WM * 4 / LW;  // copies of A per wave, buffer and fragment row
+  static constexpr int MS = (BM + BN + NTH - 1) / NTH;  // scale rows per thread
+  static constexpr int BUF = (BM + BN) * 128;
+  static constexpr int MAXG = 1024;
 
-  Tile t;
-  if (!find_tile<BM, BN>(a, ntm, ntn, t)) return;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / WN, wn = wave % WN;
-  const uint8_t* B = a.B + (a.kofs ? 0 : t.g * a.b_stride);
-  const uint8_t* Bs = a.Bs + (a.kofs ? 0 : t.g * (a.b_stride / 16));
-
-  // row of A for a row of the tile: -1 where the map points outside A
-  auto a_row = [&](int r) -> int64_t {
-    const int64_t row = t.row0 + (r < t.rows ? r : 0);
-    if (!a.a_rows) return row;
-    const int at = a.a_rows[row];
-    return at >= 0 && at < a.a_count ? at : -1;
+  struct Shared {
+    __attribute__((aligned(1024))) uint8_t buf[2][BUF];  // rows of A, then of B
+    uint2 s[2][BN + BM];      // scales of B, then of A
+    uint32_t off[BN + BM];    // offsets of the rows of B and A from their bases
+    uint8_t absent[2][BM];    // rows of C that come from nowhere, by the tile's parity
+    int first[MAXG + 1];      // row tiles before each group
   };
-  // this lane's chunk of 32 elements within a buffer's row, the same in every copy
-  const int chunk = (lane & 7) ^ (lane >> 3);
-  const uint8_t* pa[MA];
-  const uint8_t* pb[MB];
+  static_assert(sizeof(Shared) <= 160 * 1024, "LDS of a compute unit");
+
+  // Row tiles before each group, by a scan of the block.
+  static __device__ __forceinline__ void count_tiles(const MatArgs& a, int h, Shared& sh) {
+    static_assert(NTH * 2 >= MAXG, "two groups per thread");
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int n[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < MA; ++i) {
-    const int64_t row = a_row((wave + NW * i) * 8 + (lane >> 3));
-    pa[i] = row < 0 ? nullptr : a.A + row * a.lda + chunk * 16;
-  }
-#pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int64_t row = min(t.n0 + (wave + NW * i) * 8 + (lane >> 3), a.N - 1);
-    pb[i] = B + row * a.ldb + chunk * 16;
-  }
-  const uint8_t* ps[MS];
-#pragma unroll
-  for (int i = 0; i < MS; ++i) {
-    const int r = tid + NTH * i;
-    if (r < BM) {
-      const int64_t row = a_row(r);
-      ps[i] = a.As + (row < 0 ? 0 : row) * (a.lda / 16);
-    } else {
-      ps[i] = Bs + static_cast<int64_t>(min(t.n0 + r - BM, a.N - 1)) * (a.ldb / 16);
+    for (int i = 0; i < 2; ++i) {
+      const int g = 2 * tid + i;
+      if (g < a.G) n[i] = (max(group_begin(a, g + 1) - group_begin(a, g), 0) + h - 1) / h;
     }
+    int sum = n[0] + n[1];
+    for (int d = 1; d < 64; d <<= 1) {
+      const int up = __shfl_up(sum, d);
+      if (lane >= d) sum += up;
+    }
+    int* part = reinterpret_cast<int*>(sh.s);
+    if (lane == 63) part[wave] = sum;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) sum += part[w];
+    if (2 * tid < a.G) sh.first[2 * tid + 1] = sum - n[1];
+    if (2 * tid + 1 < a.G) sh.first[2 * tid + 2] = sum;
+    if (tid == 0) sh.first[0] = 0;
+    __syncthreads();
   }
 
-  uint2 sc[MS];
-  auto load_scales = [&](int kb) {
+  // Tile number tau.  Row tiles come fastest within GM of them, so that the tiles
+  // that an XCD works on at one time share their rows of A and B in its L2.
+  static __device__ __forceinline__ void find_tile(const MatArgs& a, int h, int ntm, int ntn,
+                                                   int tau, const Shared& sh, Tile& t) {
+    constexpr int GM = 4;
+    t.g = 0;
+    t.kb0 = 0;
+    t.kb1 = static_cast<int>(a.K / 32);
+    if (a.kofs) {
+      t.g = tau / (ntm * ntn);
+      tau -= t.g * (ntm * ntn);
+      // inside the operands whatever the offsets hold
+      t.kb0 = static_cast<int>(min(max(static_cast<int64_t>(a.kofs[t.g]), int64_t(0)), a.K) / 32);
+      t.kb1 =
+          static_cast<int>(min(max(static_cast<int64_t>(a.kofs[t.g + 1]), int64_t(0)), a.K) / 32);
+    }
+    const int grp = tau / (GM * ntn);
+    const int gm = min(GM, ntm - grp * GM);
+    const int r = tau - grp * GM * ntn;
+    const int m = grp * GM + r % gm;
+    t.n0 = r / gm * BN;
+    t.row0 = m * h;
+    int end = a.M;
+    if (a.off) {
+      int lo = 0, hi = a.G;  // first[lo] <= m < first[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sh.first[mid] <= m)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      t.g = lo;
+      t.row0 = group_begin(a, lo) + (m - sh.first[lo]) * h;
+      end = group_begin(a, lo + 1);
+    }
+    t.g = __builtin_amdgcn_readfirstlane(t.g);
+    t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+    t.rows = __builtin_amdgcn_readfirstlane(min(h, end - t.row0));
+    t.kb0 = __builtin_amdgcn_readfirstlane(t.kb0);
+    t.kb1 = __builtin_amdgcn_readfirstlane(t.kb1);
+  }
+
+  // The operands of a tile as the copies and scale loads go through them.
+  struct Cursor {
+    const uint8_t *base_a, *base_b;
+    global_ptr ps[MS];
+    uint4 sc[MS];  // scales of two buffers, loaded every other time
+  };
+
+  static __device__ __forceinline__ void load_scales(Cursor& cur, const Tile& t, int kb, int rows) {
 #pragma unroll
     for (int i = 0; i < MS; ++i)
-      if (tid + NTH * i < BM + BN) sc[i] = scales8(ps[i], kb, t.kb1);
-  };
-  auto copy = [&](int kb, int buf) {
-    const bool in = kb + chunk < t.kb1;
-    const int64_t at = static_cast<int64_t>(kb) * 16;
-#pragma unroll
-    for (int i = 0; i < MA; ++i) {
-      const int c = wave + NW * i;
-      if (c < AI && c * 8 < t.rows)
-        copy16_to_lds(in && pa[i] ? pa[i] + at : zero_chunk, sA[buf] + c * 1024);
-    }
-#pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      const int c = wave + NW * i;
-      if (c < BI) copy16_to_lds(in ? pb[i] + at : zero_chunk, sB[buf] + c * 1024);
-    }
-  };
-  auto put_scales = [&](int buf) {
+      if (threadIdx.x + NTH * i < rows) cur.sc[i] = scales16(cur.ps[i], kb, t.kb1);
+  }
+
+  // Scales of block kb on into the buffer: the loaded pair's first or second half.
+  static __device__ __forceinline__ void put_scales(const Cursor& cur, bool second, int buf,
+                                                    int rows, Shared& sh) {
 #pragma unroll
     for (int i = 0; i < MS; ++i)
-      if (tid + NTH * i < BM + BN) sS[buf][tid + NTH * i] = sc[i];
-  };
+      if (threadIdx.x + NTH * i < rows)
+        sh.s[buf][threadIdx.x + NTH * i] = second ? make_uint2(cur.sc[i].z, cur.sc[i].w)
+                                                  : make_uint2(cur.sc[i].x, cur.sc[i].y);
+  }
 
-  f32x16_t acc[FM][FN];
+  // The copies of the buffer from block kb on, na (at most MA) of them of A.
+  // Chunks behind the contraction's end read the first one instead.  A lane's
+  // chunk of 32 elements within a row is the same in every copy: a row's chunks
+  // are turned by (row / 2) mod 8, so that 16 rows of one chunk fill the 64
+  // banks, and a wave's copies are LW, an even number, apart.
+  template <int MA>
+  static __device__ __forceinline__ void copy(const Cursor& cur, const Tile& t, int kb, int buf,
+                                              int na, Shared& sh) {
+    static_assert(LW % 2 == 0, "one swizzle for all copies of a wave");
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (wave >= LW) return;
+    const int chunk = (lane & 7) ^ ((wave & 1) * 4 + (lane >> 4));
+    const uint32_t at = (kb + chunk < t.kb1 ? chunk : 0) * 16;
+    const uint32_t* off = sh.off + wave * 8 + (lane >> 3);
+    const uint8_t* from_a = cur.base_a + static_cast<int64_t>(kb - t.kb0) * 16;
+    const uint8_t* from_b = cur.base_b + static_cast<int64_t>(kb - t.kb0) * 16;
+    const uint32_t to_a = lds_address(sh.buf[0]) + buf * BUF + wave * 1024;
+    uint32_t ob[MB], oa[MA];
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < MB; ++i) ob[i] = off[LW * i * 8] + at;
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
+    for (int i = 0; i < MA; ++i) oa[i] = off[BN + LW * i * 8] + at;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    for (int i = 0; i < MB; ++i)
+      copy16_to_lds(from_b, ob[i], to_a + BM * 128 + LW * i * 1024);
+#pragma unroll
+    for (int i = 0; i < MA; ++i)
+      if (i < na) copy16_to_lds(from_a, oa[i], to_a + LW * i * 1024);
+  }
 
-  const int hi = lane >> 5, l31 = lane & 31;
-  // fragment i of a wave covers tile rows (i WM + wm) 32 ..: a short tile's
-  // fragments are spread evenly over the waves
-  auto frag = [&](const uint8_t* s, int row, int q) {
-    const v4i_t v =
-        *reinterpret_cast<const v4i_t*>(s + row * 128 + (((2 * q + hi) ^ (row & 7)) * 16));
-    return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
-  };
-  auto compute = [&](int buf, int left) {
-    uint2 sa[FM], sb[FN];
+  // A tile's cursor, row offsets and first copies and scale loads, into buffer
+  // buf.  Offsets from the bases fit 32 bits: a tile's rows, or (checked by the
+  // launch) all of A where rows are gathered.  A row that the map sends outside A
+  // is read as row 0 and written as zeros.
+  static __device__ __forceinline__ void begin(const MatArgs& a, const Tile& t, int buf,
+                                               uint8_t* gone, Shared& sh, Cursor& cur) {
+    const int tid = threadIdx.x;
+    const int64_t group = (a.kofs ? 0 : t.g * a.b_stride) + t.n0 * a.ldb;
+    const int64_t row0 = a.a_rows ? 0 : t.row0 * a.lda;
+    const int64_t k0 = static_cast<int64_t>(t.kb0) * 16;
+    cur.base_a = uniform_ptr(a.A + row0 + k0);
+    cur.base_b = uniform_ptr(a.B + group + k0);
+    const uint8_t* scales_a = uniform_ptr(a.As + row0 / 16);
+    const uint8_t* scales_b = uniform_ptr(a.Bs + group / 16);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      sa[i] = sS[buf][(i * WM + wm) * 32 + l31];
-      sa[i].x >>= 8 * hi;  // this half's block of a 64-element step in bytes 0 and 2
-      sa[i].y >>= 8 * hi;
+    for (int i = 0; i < MS; ++i) {
+      const int r = tid + NTH * i;
+      if (r >= BN + BM) break;
+      uint32_t row = min(r, a.N - 1 - t.n0);
+      if (r >= BN) {
+        row = r - BN < t.rows ? r - BN : 0;
+        if (a.a_rows) {
+          const int at = a.a_rows[t.row0 + row];
+          const bool none = at < 0 || at >= a.a_count;
+          row = none ? 0 : at;
+          gone[r - BN] = none;
+        }
+      }
+      const uint32_t off = row * static_cast<uint32_t>(r < BN ? a.ldb : a.lda);
+      sh.off[r] = off;
+      cur.ps[i] = (global_ptr)((r < BN ? scales_b : scales_a) + off / 16);
     }
+    __syncthreads();
+    if (t.kb0 < t.kb1) {
+      const int nf = (t.rows + 32 * WM - 1) / (32 * WM);
+      load_scales(cur, t, t.kb0, BN + nf * WM * 32);
+      copy<FM * AC>(cur, t, t.kb0, buf, nf * AC, sh);
+    }
+  }
+
+  // The products of one buffer.
+  template <int NF>
+  static __device__ __forceinline__ void compute(int buf, const Shared& sh,
+                                                 f32x16_t (&acc)[NF][FN]) {
+    const int lane = threadIdx.x & 63, hi = lane >> 5, l31 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    // fragment rows' offsets in a buffer; 64 elements further is an exclusive or
+    // with 32 q, because the swizzle only turns the chunk's number.  They are made
+    // anew for each buffer rather than kept in registers.
+    int oa = (wm * 32 + l31) * 128 + (hi ^ (l31 >> 1 & 7)) * 16;
+    int ob = (wn * FN * 32 + l31) * 128 + (hi ^ (l31 >> 1 & 7)) * 16;
+    int os = l31;
+    asm volatile("" : "+v"(oa), "+v"(ob), "+v"(os));
+    uint2 sa[NF], sb[FN];
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
-      sb[j] = sS[buf][BM + (wn * FN + j) * 32 + l31];
-      sb[j].x >>= 8 * hi;
+      sb[j] = sh.s[buf][(wn * FN + j) * 32 + os];
+      sb[j].x >>= 8 * hi;  // this half's block of a 64-element step in bytes 0 and 2
       sb[j].y >>= 8 * hi;
     }
-    auto step = [&](auto qc) {
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      sa[i] = sh.s[buf][BN + (i * WM + wm) * 32 + os];
+      sa[i].x >>= 8 * hi;
+      sa[i].y >>= 8 * hi;
+    }
+    // the fragments of the next 64 elements are read under the products of these
+    v4i_t b[2][FN], x[2][NF];
+    auto read = [&](auto qc) __attribute__((always_inline)) {
       constexpr int q = decltype(qc)::value;
-      v8i_t b[FN];
 #pragma unroll
-      for (int j = 0; j < FN; ++j) b[j] = frag(sB[buf], (wn * FN + j) * 32 + l31, q);
+      for (int j = 0; j < FN; ++j)
+        b[q & 1][j] =
+            *reinterpret_cast<const v4i_t*>(sh.buf[buf] + BM * 128 + j * 4096 + (ob ^ 32 * q));
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        if ((i * WM + wm) * 32 >= t.rows) continue;
-        const v8i_t x = frag(sA[buf], (i * WM + wm) * 32 + l31, q);
-        const int xs = static_cast<int>(q < 2 ? sa[i].x : sa[i].y);
+      for (int i = 0; i < NF; ++i)
+        x[q & 1][i] =
+            *reinterpret_cast<const v4i_t*>(sh.buf[buf] + i * WM * 4096 + (oa ^ 32 * q));
+    };
+    auto step = [&](auto qc) __attribute__((always_inline)) {
+      constexpr int q = decltype(qc)::value;
+      if constexpr (q < 3) read(std::integral_constant<int, q + 1>{});
+#pragma unroll
+      for (int i = 0; i < NF; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              x, b[j], acc[i][j], FP4, FP4, 2 * (q & 1), xs, 2 * (q & 1),
-              static_cast<int>(q < 2 ? sb[j].x : sb[j].y));
-      }
+              fp4_operand(b[q & 1][j]), fp4_operand(x[q & 1][i]), acc[i][j], FP4, FP4,
+              2 * (q & 1), static_cast<int>(q < 2 ? sb[j].x : sb[j].y), 2 * (q & 1),
+              static_cast<int>(q < 2 ? sa[i].x : sa[i].y));
+      __builtin_amdgcn_sched_barrier(0);
     };
+    read(std::integral_constant<int, 0>{});
+    __builtin_amdgcn_sched_barrier(0);
     step(std::integral_constant<int, 0>{});
-    if (left > 2) step(std::integral_constant<int, 1>{});
-    if (left > 4) step(std::integral_constant<int, 2>{});
-    if (left > 6) step(std::integral_constant<int, 3>{});
-  };
-
-  int buf = 0;
-  if (t.kb0 < t.kb1) {
-    load_scales(t.kb0);
-    copy(t.kb0, 0);
-    put_scales(0);
+    step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 3>{});
   }
-  for (int kb = t.kb0; kb < t.kb1; kb += 8, buf ^= 1) {
-    ring_wait<0>();  // this wave's copies of the buffer to be used
-    __syncthreads();  // everyone's; and everyone is done with the other buffer
-    const bool more = kb + 8 < t.kb1;
-    if (more) {
-      load_scales(kb + 8);
-      copy(kb + 8, buf ^ 1);
+
+  // All of a tile's contraction; buf is the buffer of its first copies, and on
+  // return the one that was used last.
+  template <int NF>
+  static __device__ __forceinline__ void products(const Tile& t, Cursor& cur, int& buf, Shared& sh,
+                                                  f32x16_t (&acc)[NF][FN]) {
+    constexpr int SR = BN + NF * WM * 32;  // scale rows that are used
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    bool second = false;  // of the pair of buffers whose scales were loaded
+    for (int kb = t.kb0; kb < t.kb1; kb += 8) {
+      ring_wait<0>();   // this wave's copies of the buffer to be used
+      __syncthreads();  // everyone's; and everyone is done with the other buffer
+      if (kb + 8 < t.kb1) {
+        put_scales(cur, !second, buf ^ 1, SR, sh);
+        if (!second && kb + 16 < t.kb1) load_scales(cur, t, kb + 16, SR);
+        copy<NF * AC>(cur, t, kb + 8, buf ^ 1, NF * AC, sh);
+      }
+      compute<NF>(buf, sh, acc);
+      second = !second;
+      buf ^= 1;
     }
-    compute(buf, t.kb1 - kb);
-    if (more) put_scales(buf ^ 1);
+    buf ^= 1;
   }
 
-  const int64_t base = a.kofs ? t.g * a.c_stride : 0;
+  // Writes a tile from the accumulators: one row of fragments at a time through
+  // the buffer that was used last, then whole rows, 16 bytes per lane.  A thread
+  // keeps its column.
+  template <int NF, int OUT>
+  static __device__ __forceinline__ void write(const MatArgs& a, const Tile& t, int buf,
+                                               const uint8_t* gone, Shared& sh,
+                                               const f32x16_t (&acc)[NF][FN]) {
+    typedef typename Quad<OUT>::type quad_t;
+    const int tid = threadIdx.x, lane = tid & 63, hi = lane >> 5, l31 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    constexpr int ESZ = sizeof(quad_t) / 4, ROWS = WM * 32;
+    constexpr int PITCH = BN * ESZ + 16, CPR = BN * ESZ / 16, RPS = NTH / CPR;
+    constexpr int AREA = ROWS * PITCH, AREAS = 2 * AREA <= BUF ? 2 : 1;
+    static_assert(AREA <= BUF, "staging fits a buffer");
+    static_assert(NTH % CPR == 0 && ROWS % RPS == 0, "whole rows per step");
+    const int trow = tid / CPR, tcol = tid % CPR * (16 / ESZ);
+    const int64_t ldc = a.ldc * ESZ;
+    uint8_t* dst = static_cast<uint8_t*>(a.C) +
+                   ((a.kofs ? t.g * a.c_stride : 0) + (t.row0 + trow) * a.ldc + t.n0 + tcol) * ESZ;
+    const bool whole = a.vec_out && !a.a_rows && t.n0 + BN <= a.N;
+    const uint8_t* const from = sh.buf[buf] + trow * PITCH + tcol * ESZ;
+    uint8_t* const to = sh.buf[buf] + (wm * 32 + l31) * PITCH + (wn * FN * 32 + hi * 4) * ESZ;
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
+    for (int i = 0; i < NF; ++i) {
+      const int area = i % AREAS * AREA;
+      if (AREAS == 1 && i > 0) __syncthreads();  // the rows before have been read
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int row = (i * WM + wm) * 32 + (r >> 2) * 8 + hi * 4 + (r & 3);
-      if (row >= t.rows) continue;
+      for (int j = 0; j < FN; ++j)
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int col = t.n0 + (wn * FN + j) * 32 + l31;
-        if (col < a.N) store_one(a, base + (t.row0 + static_cast<int64_t>(row)) * a.ldc + col, acc[i][j][r]);
+        for (int r = 0; r < 16; r += 4)
+          *reinterpret_cast<quad_t*>(to + area + (j * 32 + r * 2) * ESZ) =
+              Quad<OUT>::make(acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]);
+      __syncthreads();
+      if (whole) {
+#pragma unroll
+        for (int s = 0; s < ROWS; s += RPS, dst += RPS * ldc) {
+          const u32x4_t v = *reinterpret_cast<const u32x4_t*>(from + area + s * PITCH);
+          if (i * ROWS + s + trow < t.rows)
+            __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(dst));
+        }
+      } else {
+#pragma unroll 1
+        for (int s = 0; s < ROWS; s += RPS, dst += RPS * ldc) {
+          u32x4_t v = *reinterpret_cast<const u32x4_t*>(from + area + s * PITCH);
+          const int row = i * ROWS + s + trow, left = a.N - t.n0 - tcol;
+          if (row >= t.rows || left <= 0) continue;
+          if (a.a_rows && gone[row]) v = u32x4_t{0, 0, 0, 0};
+          if (a.vec_out && left >= 16 / ESZ) {
+            __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(dst));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16 / ESZ; ++e)
+              if (e < left) {
+                if constexpr (ESZ == 4)
+                  reinterpret_cast<uint32_t*>(dst)[e] = v[e];
+                else
+                  reinterpret_cast<uint16_t*>(dst)[e] =
+                      static_cast<uint16_t>(v[e / 2] >> (16 * (e & 1)));
+              }
+          }
+        }
       }
     }
+  }
+};
+
+// ntm row tiles of h rows (counted here where there are row groups), ntn column
+// tiles, problems ranges of K.  Blocks are dealt to the 8 XCDs in turn; each XCD
+// takes a consecutive eighth of the tiles, its blocks side by side.
+template <int WM, int WN, int FM, int FN, int OUT>
+__global__ __launch_bounds__(64 * WM * WN) void ring_k(MatArgs a, int h, int ntm, int ntn) {
+  typedef Ring<WM, WN, FM, FN> R;
+  __shared__ typename R::Shared sh;
+  if (a.off) {
+    R::count_tiles(a, h, sh);
+    ntm = __builtin_amdgcn_readfirstlane(sh.first[a.G]);
+  }
+  const int tiles = ntm * ntn * (a.kofs ? a.G : 1);
+  const int per = (tiles + 7) >> 3, step = gridDim.x >> 3;
+  const int last = min(tiles, static_cast<int>(blockIdx.x & 7) * per + per);
+  int tau = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (tau >= last) return;
+  Tile t;
+  typename R::Cursor cur;
+  int buf = 0, parity = 0;
+  R::find_tile(a, h, ntm, ntn, tau, sh, t);
+  R::begin(a, t, buf, sh.absent[0], sh, cur);
+  bool more = true;
+  auto body = [&](auto nfc) __attribute__((always_inline)) {
+    constexpr int NF = decltype(nfc)::value;
+    f32x16_t acc[NF][FN];
+    if (t.kb0 < t.kb1) R::put_scales(cur, false, buf, R::BN + NF * WM * 32, sh);
+    R::template products<NF>(t, cur, buf, sh, acc);
+    const Tile done = t;
+    tau += step;
+    more = tau < last;
+    if (more) {
+      // its barrier also sees every wave out of the buffer that was used last
+      R::find_tile(a, h, ntm, ntn, tau, sh, t);
+      R::begin(a, t, buf ^ 1, sh.absent[parity ^ 1], sh, cur);
+    } else {
+      __syncthreads();
+    }
+    R::template write<NF, OUT>(a, done, buf, sh.absent[parity], sh, acc);
+    buf ^= 1;
+    parity ^= 1;
+  };
+  while (more) {
+    const int nf = (t.rows + 32 * WM - 1) / (32 * WM);
+    if (nf <= 1)
+      body(std::integral_constant<int, 1>{});
+    else if (FM >= 2 && nf == 2)
+      body(std::integral_constant<int, FM >= 2 ? 2 : 1>{});
+    else if (FM >= 3 && nf == 3)
+      body(std::integral_constant<int, FM >= 3 ? 3 : 1>{});
+    else if (FM >= 4 && nf == 4)
+      body(std::integral_constant<int, FM >= 4 ? 4 : 1>{});
+    else
+      body(std::integral_constant<int, FM>{});
   }
 }
 
@@ -416,11 +648,10 @@ __global__ __launch_bounds__(64 * WN * WK) void skinny_k(MatArgs a, Unpacked u) 
           v4i_t aq;
           uint32_t as;
           a_fragment<DT>(a, u, row[i], kb + 4 * q + h, kb1, aq, as);
-          const v8i_t x = __builtin_shufflevector(aq, aq, 0, 1, 2, 3, -1, -1, -1, -1);
+          const v8i_t x = fp4_operand(aq);
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            const v8i_t y =
-                __builtin_shufflevector(bq[q][j], bq[q][j], 0, 1, 2, 3, -1, -1, -1, -1);
+            const v8i_t y = fp4_operand(bq[q][j]);
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                 x, y, acc[i][j], FP4, FP4, 0, static_cast<int>(as), 0,
                 static_cast<int>(bs[q][j]));
@@ -435,7 +666,8 @@ __global__ __launch_bounds__(64 * WN * WK) void skinny_k(MatArgs a, Unpacked u) 
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int m = m0 + 16 * i + h * 4 + r, n = n0 + 16 * j + c;
-            if (m < end && n < a.N) store_one(a, m * a.ldc + n, acc[i][j][r]);
+            if (m < end && n < a.N)
+              store_one(a, m * a.ldc + n, absent(a, m) ? 0.f : acc[i][j][r]);
           }
     } else {
       if (m0 > beg) __syncthreads();  // the last rows' sums have been read
@@ -456,22 +688,33 @@ __global__ __launch_bounds__(64 * WN * WK) void skinny_k(MatArgs a, Unpacked u) 
           sum += part[(((wo * WK + w) * MT + i) * NT + j) * 256 + at];
         const int m = m0 + 16 * i + at / 16;
         const int n = (blockIdx.x * WN + wo) * 16 * NT + 16 * j + at % 16;
-        if (m < end && n < a.N) store_one(a, m * a.ldc + n, sum);
+        if (m < end && n < a.N) store_one(a, m * a.ldc + n, absent(a, m) ? 0.f : sum);
       }
     }
   }
 }
 
+// h: rows per tile, at most the kernel's
 template <int WM, int WN, int FM, int FN>
-static int launch_ring(const MatArgs& a, hipStream_t st) {
-  constexpr int BM = WM * FM * 32, BN = WN * FN * 32;
-  // the indices of find_rows reach M / BM + G
-  const int64_t ntm = a.off ? a.M / BM + a.G : (static_cast<int64_t>(a.M) + BM - 1) / BM;
+static int launch_ring(MatArgs a, int h, hipStream_t st) {
+  constexpr int BN = WN * FN * 32;
+  const int64_t ntm = a.off ? a.M / h + a.G : (static_cast<int64_t>(a.M) + h - 1) / h;  // at most
   const int64_t ntn = (static_cast<int64_t>(a.N) + BN - 1) / BN;
   const int64_t tiles = ntm * ntn * (a.kofs ? a.G : 1);
-  if (tiles + 7 > 0x7fffffff) return MOE_EUNSUPPORTED;
-  hipLaunchKernelGGL((ring_k<WM, WN, FM, FN>), dim3(static_cast<unsigned>((tiles + 7) / 8 * 8)),
-                     dim3(64 * WM * WN), 0, st, a, static_cast<int>(ntm), static_cast<int>(ntn));
+  if (tiles > 0x7fff0000) return MOE_EUNSUPPORTED;
+  const int esz = a.out == MOE_F32 ? 4 : 2;
+  a.vec_out = reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && a.ldc * esz % 16 == 0 &&
+              a.c_stride * esz % 16 == 0;
+  // one block per compute unit, or per tile where there are fewer
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(256, (tiles + 7) / 8 * 8)));
+  const dim3 block(64 * WM * WN);
+  const int tm = static_cast<int>(ntm), tn = static_cast<int>(ntn);
+  if (a.out == MOE_F32)
+    hipLaunchKernelGGL((ring_k<WM, WN, FM, FN, MOE_F32>), grid, block, 0, st, a, h, tm, tn);
+  else if (a.out == MOE_BF16)
+    hipLaunchKernelGGL((ring_k<WM, WN, FM, FN, MOE_BF16>), grid, block, 0, st, a, h, tm, tn);
+  else
+    hipLaunchKernelGGL((ring_k<WM, WN, FM, FN, MOE_F16>), grid, block, 0, st, a, h, tm, tn);
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }
@@ -505,12 +748,38 @@ static int skinny(const MatArgs& a, const Unpacked& u, int64_t per_group, hipStr
 // kernel is taken.
 constexpr int SKINNY_ROWS = 32;
 
+// Tile height: the multiple of 64 up to 320 whose tiles cover the rows of a
+// problem with the least work per compute unit, the taller one on a tie (fewer
+// reads of B).
+static int tile_height(int64_t rows, int64_t problems, int64_t N) {
+  int best = 64;
+  int64_t cost = 0;
+  for (int h = 64; h <= 320; h += 64) {
+    const int64_t tiles = (rows + h - 1) / h * ((N + 255) / 256) * problems;
+    const int64_t c = (tiles + 255) / 256 * (h + 128);
+    if (h == 64 || c <= cost) {
+      best = h;
+      cost = c;
+    }
+  }
+  return best;
+}
+
+// The ring kernel's offsets: 320 rows of A or B, or all of A if its rows are
+// gathered, within 4 GiB.
+static bool ring_fits(const MatArgs& a) {
+  const int64_t limit = int64_t(1) << 32;
+  return 320 * std::max(a.lda, a.ldb) < limit &&
+         (!a.a_rows || static_cast<int64_t>(a.a_count) * a.lda < limit);
+}
+
 static int product(const MatArgs& a, hipStream_t st) {
-  if (a.kofs) return launch_ring<2, 4, 4, 2>(a, st);
+  if (a.kofs)
+    return ring_fits(a) ? launch_ring<2, 4, 5, 2>(a, tile_height(a.M, a.G, a.N), st)
+                        : MOE_EUNSUPPORTED;
   const int64_t per = a.off ? (a.M + a.G - 1) / a.G : a.M;
-  if (per <= SKINNY_ROWS) return skinny<-1>(a, Unpacked{}, per, st);
-  if (per <= 128) return launch_ring<1, 8, 4, 1>(a, st);
-  return launch_ring<2, 4, 4, 2>(a, st);
+  if (per <= SKINNY_ROWS || !ring_fits(a)) return skinny<-1>(a, Unpacked{}, per, st);
+  return launch_ring<2, 4, 5, 2>(a, tile_height(per, a.off ? a.G : 1, a.N), st);
 }
 
 static bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -593,9 +862,9 @@ extern "C" int moe_mxfp4_matmul_kgroup(const uint8_t* a_codes, const uint8_t* a_
   a.ldc = N;
   a.c_stride = M * N;
   a.out = out_dtype;
-  // one range: an ordinary product (an empty one still writes its zeros)
-  return k_offsets || K == 0 ? launch_ring<2, 4, 4, 2>(a, static_cast<hipStream_t>(stream))
-                             : product(a, static_cast<hipStream_t>(stream));
+  // an empty contraction still writes its zeros
+  if (K == 0) return launch_ring<2, 4, 5, 2>(a, 64, static_cast<hipStream_t>(stream));
+  return product(a, static_cast<hipStream_t>(stream));
 }
 
 extern "C" size_t moe_mxfp4_linear_workspace_bytes(int64_t rows, int64_t K) {
