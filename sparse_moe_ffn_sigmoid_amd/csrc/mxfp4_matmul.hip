@@ -551,39 +551,64 @@ __global__ __launch_bounds__(64 * WM * WN) void ring_k(MatArgs a, int h, int ntm
 // A few rows per problem.  A block takes 16 NT columns per wave group and all of
 // a group's rows, 16 MT at a time; WK waves split the contraction into stretches
 // of 256 elements dealt in turn and add their sums through LDS in a fixed order.
-// Lane (c, h), c = lane mod 16, h = lane / 16, holds elements [32 h, 32 h + 32)
-// of a 128-element step of row c: one block with its scale.
+// The matrix instruction multiplies 128 elements, lane (c, h), c = lane mod 16,
+// h = lane / 16, holding one block of 32 of row c with its scale.  Which blocks
+// meet in one instruction is free as long as both operands agree: lane h takes
+// blocks 2 h and 2 h + 1 of a stretch, so that its codes are 32 consecutive bytes,
+// four lanes read a whole cache line and the scales are two bytes.  U stretches
+// are loaded before the first is multiplied.
 struct Unpacked {  // activations to be packed on the way in
   const void* x;
   int64_t stride;
 };
 
-template <int DT>  // -1: A is packed
-__device__ __forceinline__ void a_fragment(const MatArgs& a, const Unpacked& u, int64_t row,
-                                           int kb, int kb1, v4i_t& q, uint32_t& s) {
-  q = v4i_t{0, 0, 0, 0};
-  s = 127u;
-  if (row < 0 || kb >= kb1) return;
-  if constexpr (DT < 0) {
-    q = *reinterpret_cast<const v4i_t*>(a.A + row * a.lda + static_cast<int64_t>(kb) * 16);
-    s = a.As[row * (a.lda / 16) + kb];
+// Two blocks of a row from block kb on: codes and scales (in bytes 0 and 1).
+// Blocks at or behind kb1, and a row that is not there, are codes of zero.
+__device__ __forceinline__ void load_pair(const uint8_t* codes, const uint8_t* scales, int kb,
+                                          int kb1, bool there, v4i_t (&q)[2], uint32_t& s) {
+  q[0] = q[1] = v4i_t{0, 0, 0, 0};
+  s = 0x7f7fu;
+  if (!there || kb >= kb1) return;
+  const v4i_t* p = reinterpret_cast<const v4i_t*>(codes + static_cast<int64_t>(kb) * 16);
+  q[0] = p[0];
+  if (kb + 1 < kb1) {
+    struct __attribute__((packed, aligned(1))) Two {
+      uint16_t v;
+    };
+    q[1] = p[1];
+    s = reinterpret_cast<const Two*>(scales + kb)->v;
   } else {
-    float v[4][8];
-    uint32_t m = 0;
-    const auto* p = static_cast<const typename Elem<DT>::type*>(u.x) + row * u.stride +
-                    static_cast<int64_t>(kb) * 32;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      load8<DT>(p + 8 * i, 8, true, v[i]);
-      m = max(m, amax8(v[i]));
-    }
-    s = scale_byte(m);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = static_cast<int>(encode8(v[i], s));
+    s = 0x7f00u | scales[kb];
   }
 }
 
-template <int WN, int WK, int NT, int MT, int DT>
+// The same of unpacked values, packed here.
+template <int DT>
+__device__ __forceinline__ void pack_pair(const Unpacked& u, int64_t row, int kb, int kb1,
+                                          v4i_t (&q)[2], uint32_t& s) {
+  q[0] = q[1] = v4i_t{0, 0, 0, 0};
+  s = 0x7f7fu;
+  if (row < 0) return;
+  const auto* p = static_cast<const typename Elem<DT>::type*>(u.x) + row * u.stride;
+  uint32_t sb[2] = {127u, 127u};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (kb + k >= kb1) break;
+    float v[4][8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      load8<DT>(p + static_cast<int64_t>(kb + k) * 32 + 8 * i, 8, true, v[i]);
+      m = max(m, amax8(v[i]));
+    }
+    sb[k] = scale_byte(m);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[k][i] = static_cast<int>(encode8(v[i], sb[k]));
+  }
+  s = sb[0] | (sb[1] << 8);
+}
+
+template <int WN, int WK, int NT, int MT, int U, int DT>  // DT -1: A is packed
 __global__ __launch_bounds__(64 * WN * WK) void skinny_k(MatArgs a, Unpacked u) {
   constexpr int NW = WN * WK;
   __shared__ float part[WK > 1 ? WK * WN * NT * MT * 256 : 1];
@@ -607,8 +632,8 @@ __global__ __launch_bounds__(64 * WN * WK) void skinny_k(MatArgs a, Unpacked u) 
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int64_t n = min(n0 + 16 * j + c, a.N - 1);
-    pb[j] = B + n * a.ldb + h * 16;
-    ps[j] = Bs + n * (a.ldb / 16) + h;
+    pb[j] = B + n * a.ldb;
+    ps[j] = Bs + n * (a.ldb / 16);
   }
   for (int m0 = beg; m0 < end; m0 += 16 * MT) {
     f32x4_t acc[MT][NT];
@@ -624,39 +649,38 @@ __global__ __launch_bounds__(64 * WN * WK) void skinny_k(MatArgs a, Unpacked u) 
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
-    for (int kb = wk * 8; kb < kb1; kb += WK * 8) {
-      v4i_t bq[2][NT];
-      uint32_t bs[2][NT];
+    for (int k0 = wk * 8; k0 < kb1; k0 += WK * U * 8) {
+      v4i_t bq[U][NT][2], aq[U][MT][2];
+      uint32_t bs[U][NT], as[U][MT];
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+      for (int v = 0; v < U; ++v)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const bool in = kb + 4 * q + h < kb1;
-          bq[q][j] = v4i_t{0, 0, 0, 0};
-          bs[q][j] = 127u;
-          if (in) {
-            bq[q][j] = __builtin_nontemporal_load(
-                reinterpret_cast<const v4i_t*>(pb[j] + static_cast<int64_t>(kb + 4 * q) * 16));
-            bs[q][j] = ps[j][kb + 4 * q];
-          }
-        }
+        for (int j = 0; j < NT; ++j)
+          load_pair(pb[j], ps[j], k0 + v * WK * 8 + 2 * h, kb1, true, bq[v][j], bs[v][j]);
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+      for (int v = 0; v < U; ++v)
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-          if (m0 + 16 * i >= end) continue;
-          v4i_t aq;
-          uint32_t as;
-          a_fragment<DT>(a, u, row[i], kb + 4 * q + h, kb1, aq, as);
-          const v8i_t x = fp4_operand(aq);
+          const int kb = k0 + v * WK * 8 + 2 * h;
+          if constexpr (DT < 0)
+            load_pair(a.A + row[i] * a.lda, a.As + row[i] * (a.lda / 16), kb, kb1, row[i] >= 0,
+                      aq[v][i], as[v][i]);
+          else
+            pack_pair<DT>(u, row[i], kb, kb1, aq[v][i], as[v][i]);
+        }
+#pragma unroll
+      for (int v = 0; v < U; ++v)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            const v8i_t y = fp4_operand(bq[q][j]);
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                x, y, acc[i][j], FP4, FP4, 0, static_cast<int>(as), 0,
-                static_cast<int>(bs[q][j]));
+                fp4_operand(aq[v][i][0]), fp4_operand(bq[v][j][0]), acc[i][j], FP4, FP4, 0,
+                static_cast<int>(as[v][i]), 0, static_cast<int>(bs[v][j]));
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                fp4_operand(aq[v][i][1]), fp4_operand(bq[v][j][1]), acc[i][j], FP4, FP4, 1,
+                static_cast<int>(as[v][i]), 1, static_cast<int>(bs[v][j]));
           }
-        }
     }
     if constexpr (WK == 1) {
 #pragma unroll
@@ -719,10 +743,10 @@ static int launch_ring(MatArgs a, int h, hipStream_t st) {
   return MOE_OK;
 }
 
-template <int WN, int WK, int NT, int MT, int DT>
+template <int WN, int WK, int NT, int MT, int U, int DT>
 static int launch_skinny(const MatArgs& a, const Unpacked& u, hipStream_t st) {
   const int64_t per = 16ll * NT * WN;
-  hipLaunchKernelGGL((skinny_k<WN, WK, NT, MT, DT>),
+  hipLaunchKernelGGL((skinny_k<WN, WK, NT, MT, U, DT>),
                      dim3(static_cast<unsigned>((a.N + per - 1) / per),
                           static_cast<unsigned>(a.off ? a.G : 1)),
                      dim3(64 * WN * WK), 0, st, a, u);
@@ -736,12 +760,15 @@ static int skinny(const MatArgs& a, const Unpacked& u, int64_t per_group, hipStr
   const int64_t waves = (static_cast<int64_t>(a.N) + 15) / 16 * (a.off ? a.G : 1);
   if constexpr (DT < 0) {
     if (per_group > 16) {
-      if (waves >= 8192) return launch_skinny<4, 1, 1, 4, DT>(a, u, st);
-      return launch_skinny<1, 8, 1, 4, DT>(a, u, st);
+      if (waves >= 8192) return launch_skinny<4, 1, 1, 4, 1, DT>(a, u, st);
+      return launch_skinny<1, 8, 1, 4, 1, DT>(a, u, st);
     }
+    if (waves >= 8192) return launch_skinny<4, 1, 1, 1, 4, DT>(a, u, st);
+    return launch_skinny<1, 8, 1, 1, 2, DT>(a, u, st);
+  } else {
+    if (waves >= 8192) return launch_skinny<4, 1, 1, 1, 1, DT>(a, u, st);
+    return launch_skinny<1, 8, 1, 1, 1, DT>(a, u, st);
   }
-  if (waves >= 8192) return launch_skinny<4, 1, 1, 1, DT>(a, u, st);
-  return launch_skinny<1, 8, 1, 1, DT>(a, u, st);
 }
 
 // Rows per problem up to which the codes of B bound the time and the skinny
