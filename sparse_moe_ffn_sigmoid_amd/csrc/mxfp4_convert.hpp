@@ -97,5 +97,11 @@ __device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {
   return m;
 }
 
+// max over the four lanes of a block of a row
+__device__ __forceinline__ uint32_t max4(uint32_t m) {
+  m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 1, 4)));
+  return max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 2, 4)));
+}
+
 }  // namespace mx
 }  // namespace moe

@@ -557,11 +557,6 @@ __global__ __launch_bounds__(64 * WM * WN) void ring_k(MatArgs a, int h, int ntm
 // blocks 2 h and 2 h + 1 of a stretch, so that its codes are 32 consecutive bytes,
 // four lanes read a whole cache line and the scales are two bytes.  U stretches
 // are loaded before the first is multiplied.
-struct Unpacked {  // activations to be packed on the way in
-  const void* x;
-  int64_t stride;
-};
-
 // Two blocks of a row from block kb on: codes and scales (in bytes 0 and 1).
 // Blocks at or behind kb1, and a row that is not there, are codes of zero.
 __device__ __forceinline__ void load_pair(const uint8_t* codes, const uint8_t* scales, int kb,
@@ -582,34 +577,8 @@ __device__ __forceinline__ void load_pair(const uint8_t* codes, const uint8_t* s
   }
 }
 
-// The same of unpacked values, packed here.
-template <int DT>
-__device__ __forceinline__ void pack_pair(const Unpacked& u, int64_t row, int kb, int kb1,
-                                          v4i_t (&q)[2], uint32_t& s) {
-  q[0] = q[1] = v4i_t{0, 0, 0, 0};
-  s = 0x7f7fu;
-  if (row < 0) return;
-  const auto* p = static_cast<const typename Elem<DT>::type*>(u.x) + row * u.stride;
-  uint32_t sb[2] = {127u, 127u};
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (kb + k >= kb1) break;
-    float v[4][8];
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      load8<DT>(p + static_cast<int64_t>(kb + k) * 32 + 8 * i, 8, true, v[i]);
-      m = max(m, amax8(v[i]));
-    }
-    sb[k] = scale_byte(m);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[k][i] = static_cast<int>(encode8(v[i], sb[k]));
-  }
-  s = sb[0] | (sb[1] << 8);
-}
-
-template <int WN, int WK, int NT, int MT, int U, int DT>  // DT -1: A is packed
-__global__ __launch_bounds__(64 * WN * WK) void skinny_k(MatArgs a, Unpacked u) {
+template <int WN, int WK, int NT, int MT, int U>
+__global__ __launch_bounds__(64 * WN * WK) void skinny_k(MatArgs a) {
   constexpr int NW = WN * WK;
   __shared__ float part[WK > 1 ? WK * WN * NT * MT * 256 : 1];
   const int lane = threadIdx.x & 63;
@@ -661,12 +630,9 @@ __global__ __launch_bounds__(64 * WN * WK) void skinny_k(MatArgs a, Unpacked u) 
       for (int v = 0; v < U; ++v)
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-          const int kb = k0 + v * WK * 8 + 2 * h;
-          if constexpr (DT < 0)
-            load_pair(a.A + row[i] * a.lda, a.As + row[i] * (a.lda / 16), kb, kb1, row[i] >= 0,
-                      aq[v][i], as[v][i]);
-          else
-            pack_pair<DT>(u, row[i], kb, kb1, aq[v][i], as[v][i]);
+          const int64_t r = row[i] < 0 ? 0 : row[i];
+          load_pair(a.A + r * a.lda, a.As + r * (a.lda / 16), k0 + v * WK * 8 + 2 * h, kb1,
+                    row[i] >= 0, aq[v][i], as[v][i]);
         }
 #pragma unroll
       for (int v = 0; v < U; ++v)
@@ -718,6 +684,96 @@ __global__ __launch_bounds__(64 * WN * WK) void skinny_k(MatArgs a, Unpacked u) 
   }
 }
 
+// At most 16 rows of activations as they are: the block packs them into LDS while
+// its first codes of the weights are on the way, then goes on as skinny_k.  One
+// launch for a token, whose time is the launch and one trip to memory.
+constexpr int FUSED_WAVES = 8, FUSED_U = 4;
+
+template <int DT>
+__global__ __launch_bounds__(64 * FUSED_WAVES) void fused_k(MatArgs a, const void* x,
+                                                            int64_t stride) {
+  constexpr int WK = FUSED_WAVES, U = FUSED_U;
+  __shared__ float part[WK * 256];
+  // codes of the rows, each followed by 32 bytes that keep rows off one
+  // another's banks, then their scales
+  extern __shared__ __attribute__((aligned(16))) uint8_t packed[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 15, h = lane >> 4;
+  const int kb1 = static_cast<int>(a.K / 32), pitch = kb1 * 16 + 32;
+  uint8_t* const scales = packed + a.M * pitch;
+  const int n0 = blockIdx.x * 16;
+  const int64_t n = min(n0 + c, a.N - 1);
+  const uint8_t *pb = a.B + n * a.ldb, *ps = a.Bs + n * (a.ldb / 16);
+  f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  v4i_t bq[U][2];
+  uint32_t bs[U];
+  auto load = [&](int k0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int v = 0; v < U; ++v)
+      load_pair(pb, ps, k0 + v * WK * 8 + 2 * h, kb1, true, bq[v], bs[v]);
+  };
+  load(wave * 8);
+  // eight elements a thread, four threads a block of 32
+  for (int i = tid; i < a.M * kb1 * 4; i += 64 * WK) {
+    const int m = i / (kb1 * 4), e = i - m * (kb1 * 4);
+    const int at = a.a_rows ? a.a_rows[m] : m;
+    const int64_t row = at >= 0 && at < a.a_count ? at : 0;
+    float v[8];
+    load8<DT>(static_cast<const typename Elem<DT>::type*>(x) + row * stride + e * 8, 8, true, v);
+    const uint32_t sb = scale_byte(max4(amax8(v)));
+    *reinterpret_cast<uint32_t*>(packed + m * pitch + e * 4) = encode8(v, sb);
+    if ((e & 3) == 0) scales[m * kb1 + (e >> 2)] = static_cast<uint8_t>(sb);
+  }
+  __syncthreads();
+  for (int k0 = wave * 8;;) {
+#pragma unroll
+    for (int v = 0; v < U; ++v) {
+      v4i_t aq[2] = {v4i_t{0, 0, 0, 0}, v4i_t{0, 0, 0, 0}};
+      uint32_t as = 0x7f7fu;
+      const int kb = k0 + v * WK * 8 + 2 * h;
+      if (c < a.M && kb < kb1) {
+        const int second = min(kb + 1, kb1 - 1);  // its partner's codes are zero there
+        aq[0] = *reinterpret_cast<const v4i_t*>(packed + c * pitch + kb * 16);
+        aq[1] = *reinterpret_cast<const v4i_t*>(packed + c * pitch + second * 16);
+        as = scales[c * kb1 + kb] | (static_cast<uint32_t>(scales[c * kb1 + second]) << 8);
+      }
+      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+          fp4_operand(aq[0]), fp4_operand(bq[v][0]), acc, FP4, FP4, 0, static_cast<int>(as), 0,
+          static_cast<int>(bs[v]));
+      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+          fp4_operand(aq[1]), fp4_operand(bq[v][1]), acc, FP4, FP4, 1, static_cast<int>(as), 1,
+          static_cast<int>(bs[v]));
+    }
+    k0 += WK * U * 8;
+    if (k0 >= kb1) break;
+    load(k0);
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) part[wave * 256 + (h * 4 + r) * 16 + c] = acc[r];
+  __syncthreads();
+  if (tid < a.M * 16 && n0 + tid % 16 < a.N) {
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < WK; ++w) sum += part[w * 256 + tid];
+    const int m = tid / 16;
+    store_one(a, m * a.ldc + n0 + tid % 16, absent(a, m) ? 0.f : sum);
+  }
+}
+
+// LDS of fused_k's packed rows; it takes what leaves a second block room.
+static int64_t fused_bytes(int64_t M, int64_t K) { return M * (K / 2 + 32 + K / 32); }
+constexpr int64_t FUSED_BYTES = 64 << 10;
+
+template <int DT>
+static int launch_fused(const MatArgs& a, const void* x, int64_t stride, hipStream_t st) {
+  hipLaunchKernelGGL(fused_k<DT>, dim3(static_cast<unsigned>((a.N + 15ll) / 16)),
+                     dim3(64 * FUSED_WAVES), static_cast<unsigned>(fused_bytes(a.M, a.K)), st, a, x,
+                     stride);
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
 // h: rows per tile, at most the kernel's
 template <int WM, int WN, int FM, int FN>
 static int launch_ring(MatArgs a, int h, hipStream_t st) {
@@ -743,32 +799,23 @@ static int launch_ring(MatArgs a, int h, hipStream_t st) {
   return MOE_OK;
 }
 
-template <int WN, int WK, int NT, int MT, int U, int DT>
-static int launch_skinny(const MatArgs& a, const Unpacked& u, hipStream_t st) {
+template <int WN, int WK, int NT, int MT, int U>
+static int launch_skinny(const MatArgs& a, hipStream_t st) {
   const int64_t per = 16ll * NT * WN;
-  hipLaunchKernelGGL((skinny_k<WN, WK, NT, MT, U, DT>),
+  hipLaunchKernelGGL((skinny_k<WN, WK, NT, MT, U>),
                      dim3(static_cast<unsigned>((a.N + per - 1) / per),
                           static_cast<unsigned>(a.off ? a.G : 1)),
-                     dim3(64 * WN * WK), 0, st, a, u);
+                     dim3(64 * WN * WK), 0, st, a);
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }
 
-template <int DT>
-static int skinny(const MatArgs& a, const Unpacked& u, int64_t per_group, hipStream_t st) {
+static int skinny(const MatArgs& a, int64_t per_group, hipStream_t st) {
   // waves that a split over columns alone gives
   const int64_t waves = (static_cast<int64_t>(a.N) + 15) / 16 * (a.off ? a.G : 1);
-  if constexpr (DT < 0) {
-    if (per_group > 16) {
-      if (waves >= 8192) return launch_skinny<4, 1, 1, 4, 1, DT>(a, u, st);
-      return launch_skinny<1, 8, 1, 4, 1, DT>(a, u, st);
-    }
-    if (waves >= 8192) return launch_skinny<4, 1, 1, 1, 4, DT>(a, u, st);
-    return launch_skinny<1, 8, 1, 1, 2, DT>(a, u, st);
-  } else {
-    if (waves >= 8192) return launch_skinny<4, 1, 1, 1, 1, DT>(a, u, st);
-    return launch_skinny<1, 8, 1, 1, 1, DT>(a, u, st);
-  }
+  if (per_group > 16)
+    return waves >= 8192 ? launch_skinny<4, 1, 1, 4, 1>(a, st) : launch_skinny<1, 8, 1, 4, 1>(a, st);
+  return waves >= 8192 ? launch_skinny<4, 1, 1, 1, 4>(a, st) : launch_skinny<1, 8, 1, 1, 4>(a, st);
 }
 
 // Rows per problem up to which the codes of B bound the time and the skinny
@@ -805,7 +852,7 @@ static int product(const MatArgs& a, hipStream_t st) {
     return ring_fits(a) ? launch_ring<2, 4, 5, 2>(a, tile_height(a.M, a.G, a.N), st)
                         : MOE_EUNSUPPORTED;
   const int64_t per = a.off ? (a.M + a.G - 1) / a.G : a.M;
-  if (per <= SKINNY_ROWS || !ring_fits(a)) return skinny<-1>(a, Unpacked{}, per, st);
+  if (per <= SKINNY_ROWS || !ring_fits(a)) return skinny(a, per, st);
   return launch_ring<2, 4, 5, 2>(a, tile_height(per, a.off ? a.G : 1, a.N), st);
 }
 
@@ -924,7 +971,8 @@ extern "C" int moe_mxfp4_linear(const void* x, int32_t x_dtype, int64_t x_rows,
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MOE_EINVAL;
   if (workspace_bytes < moe_mxfp4_linear_workspace_bytes(x_rows, K)) return MOE_EWORKSPACE;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (!row_offsets && M <= 16 && aligned16(x) && row_stride * size % 16 == 0) {
+  if (!row_offsets && M <= 16 && fused_bytes(M, K) <= FUSED_BYTES && aligned16(x) &&
+      row_stride * size % 16 == 0) {
     MatArgs a{};
     a.B = w_codes;
     a.Bs = w_scales;
@@ -938,10 +986,9 @@ extern "C" int moe_mxfp4_linear(const void* x, int32_t x_dtype, int64_t x_rows,
     a.C = out;
     a.ldc = ld_out;
     a.out = out_dtype;
-    const Unpacked u{x, row_stride};
-    if (x_dtype == MOE_F32) return skinny<MOE_F32>(a, u, M, st);
-    if (x_dtype == MOE_BF16) return skinny<MOE_BF16>(a, u, M, st);
-    return skinny<MOE_F16>(a, u, M, st);
+    if (x_dtype == MOE_F32) return launch_fused<MOE_F32>(a, x, row_stride, st);
+    if (x_dtype == MOE_BF16) return launch_fused<MOE_BF16>(a, x, row_stride, st);
+    return launch_fused<MOE_F16>(a, x, row_stride, st);
   }
   moe::Carver cv(workspace);
   uint8_t* codes = cv.take<uint8_t>(x_rows * (K / 2));

@@ -34,12 +34,6 @@ struct PackArgs {
   int G;
 };
 
-// max over the four lanes of a block of a row
-__device__ __forceinline__ uint32_t max4(uint32_t m) {
-  m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 1, 4)));
-  return max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 2, 4)));
-}
-
 // Rows only: a wave takes 512 consecutive elements of a row (8 per lane, four
 // lanes to a block) and ROWS_PER rows one after the other.
 constexpr int ROWS_PER = 4;
