@@ -281,9 +281,13 @@ def _device_of(t, name):
     return t.device
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _call(fn, dev, *args):
     """fn(*args, stream) on the device's current stream; raises MoeError."""
-    stream = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
     if dev.index == torch.cuda.current_device():
         st = fn(*args, stream)
     else:
@@ -352,9 +356,9 @@ def balance_loss(scores: torch.Tensor, idx: torch.Tensor, seq_offsets=None, toke
     if want_grad:
         out["dscores"] = torch.empty((T, n), dtype=torch.float32, device=dev)
     ws = _workspace(workspace, _lib.moe_balance_loss_workspace_bytes(T, S), dev)
-    _call(_lib.moe_balance_loss, dev, _ptr(scores), ld, T, n, k, _ptr(idx), _ptr(seq_offsets), S,
-          _ptr(mask), _ptr(dloss), _ptr(out["loss"]), _ptr(out["counts"]), _ptr(out["tokens"]),
-          _ptr(out.get("dscores")), _ptr(ws), ws.numel())
+    _call(_lib.moe_balance_loss, dev, _addr(scores), ld, T, n, k, _addr(idx), _addr(seq_offsets), S,
+          _addr(mask), _addr(dloss), _addr(out["loss"]), _addr(out["counts"]), _addr(out["tokens"]),
+          _addr(out.get("dscores")), _addr(ws), ws.numel())
     return out
 
 
@@ -367,8 +371,8 @@ def balance_loss_backward(scores: torch.Tensor, counts: torch.Tensor, tokens: to
     _check(counts, "counts", torch.int32, (S, n), dev)
     _check(tokens, "tokens", torch.int32, (S,), dev)
     dscores = torch.empty((T, n), dtype=torch.float32, device=dev)
-    _call(_lib.moe_balance_loss_backward, dev, _ptr(scores), ld, T, n, k, _ptr(counts),
-          _ptr(tokens), _ptr(seq_offsets), S, _ptr(mask), _ptr(dloss), _ptr(dscores))
+    _call(_lib.moe_balance_loss_backward, dev, _addr(scores), ld, T, n, k, _addr(counts),
+          _addr(tokens), _addr(seq_offsets), S, _addr(mask), _addr(dloss), _addr(dscores))
     return dscores
 
 
@@ -401,8 +405,8 @@ def router_backward(x: torch.Tensor, w_router: torch.Tensor, scores: torch.Tenso
                 _check(into[f], f, dt, shape, dev)
     need = _lib.moe_router_backward_workspace_bytes(T, d, n)
     ws = _workspace(workspace, need, dev)
-    _call(_lib.moe_router_backward, dev, _ptr(x), _ptr(w_router), _ptr(scores), _ptr(dscores), T,
-          d, n, 0 if into is None else 1, *[_ptr(out.get(f)) for f in names], _ptr(ws),
+    _call(_lib.moe_router_backward, dev, _addr(x), _addr(w_router), _addr(scores), _addr(dscores), T,
+          d, n, 0 if into is None else 1, *[_addr(out.get(f)) for f in names], _addr(ws),
           ws.numel())
     return out
 
@@ -477,9 +481,9 @@ def mxfp4_pack(x: torch.Tensor, rows: bool = True, cols: bool = False, offsets=N
         out["scales_t"] = torch.empty(lead + (K, padded // 32), dtype=torch.uint8, device=dev)
     if offsets is not None:
         out["offsets_t"] = torch.empty(G + 1, dtype=torch.int32, device=dev)
-    _call(_lib.moe_mxfp4_pack, dev, _ptr(x), dt, B, R, K, rs, bs,
-          *[_ptr(out.get(f)) for f in ("codes", "scales", "codes_t", "scales_t")], _ptr(offsets),
-          G, _ptr(out.get("offsets_t")))
+    _call(_lib.moe_mxfp4_pack, dev, _addr(x), dt, B, R, K, rs, bs,
+          *[_addr(out.get(f)) for f in ("codes", "scales", "codes_t", "scales_t")], _addr(offsets),
+          G, _addr(out.get("offsets_t")))
     return out
 
 
@@ -492,8 +496,8 @@ def mxfp4_unpack(codes: torch.Tensor, scales: torch.Tensor, K: int, dtype=torch.
     if len(shape) < 2 or not shape[-1] - 32 < K <= shape[-1]:
         raise ValueError(f"K = {K} does not fit codes of {shape[-1]} elements")
     out = torch.empty(shape[:-1] + (K,), dtype=dtype, device=dev)
-    _call(_lib.moe_mxfp4_unpack, dev, _ptr(codes), _ptr(scales), out.numel() // K, K, dt,
-          _ptr(out), K)
+    _call(_lib.moe_mxfp4_unpack, dev, _addr(codes), _addr(scales), out.numel() // K, K, dt,
+          _addr(out), K)
     return out
 
 
@@ -538,8 +542,8 @@ def mxfp4_matmul(a_codes, a_scales, b_codes, b_scales, offsets=None, rows=None,
         _check(rows, "rows", torch.int32, (M,), dev)
     dt = _mx_type(out_dtype, "out_dtype")
     out, ldo = _mx_out(out, M, N, out_dtype, dev)
-    _call(_lib.moe_mxfp4_matmul, dev, _ptr(a_codes), _ptr(a_scales), R, _ptr(b_codes),
-          _ptr(b_scales), M, N, K, _ptr(offsets), G, _ptr(rows), _ptr(out), dt, ldo)
+    _call(_lib.moe_mxfp4_matmul, dev, _addr(a_codes), _addr(a_scales), R, _addr(b_codes),
+          _addr(b_scales), M, N, K, _addr(offsets), G, _addr(rows), _addr(out), dt, ldo)
     return out
 
 
@@ -561,8 +565,8 @@ def mxfp4_matmul_kgroup(a_codes, a_scales, b_codes, b_scales, offsets=None,
         G = offsets.numel() - 1
         _check(offsets, "offsets", torch.int32, (G + 1,), dev)
     out = torch.empty(((G,) if offsets is not None else ()) + (M, N), dtype=out_dtype, device=dev)
-    _call(_lib.moe_mxfp4_matmul_kgroup, dev, _ptr(a_codes), _ptr(a_scales), _ptr(b_codes),
-          _ptr(b_scales), M, N, K, _ptr(offsets), G, _ptr(out), dt)
+    _call(_lib.moe_mxfp4_matmul_kgroup, dev, _addr(a_codes), _addr(a_scales), _addr(b_codes),
+          _addr(b_scales), M, N, K, _addr(offsets), G, _addr(out), dt)
     return out
 
 
@@ -591,8 +595,8 @@ def mxfp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
     dt = _mx_type(out_dtype, "out_dtype")
     out, ldo = _mx_out(out, M, N, out_dtype, dev)
     ws = _workspace(workspace, _lib.moe_mxfp4_linear_workspace_bytes(R, K), dev)
-    _call(_lib.moe_mxfp4_linear, dev, _ptr(x), xt, R, rs, _ptr(w_codes), _ptr(w_scales), M, N, K,
-          _ptr(offsets), G, _ptr(rows), _ptr(out), dt, ldo, _ptr(ws), ws.numel())
+    _call(_lib.moe_mxfp4_linear, dev, _addr(x), xt, R, rs, _addr(w_codes), _addr(w_scales), M, N, K,
+          _addr(offsets), G, _addr(rows), _addr(out), dt, ldo, _addr(ws), ws.numel())
     return out
 
 

@@ -284,6 +284,62 @@ __global__ __launch_bounds__(256) void finish_k(Args a) {
   }
 }
 
+// A small batch in one launch of one block: for each sequence the counts stay
+// in LDS and its tokens are dealt to the waves.  The row arithmetic is pass_k's.
+constexpr int SMALL_WAVES = 16;
+
+template <int VEC, int NV>
+__global__ __launch_bounds__(64 * SMALL_WAVES) void small_k(Args a) {
+  __shared__ int32_t hist[MAXN + 1];
+  __shared__ float red[SMALL_WAVES];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int done = 0;  // tokens before this one have their gradients
+  for (int s = 0; s < a.S; ++s) {
+    const int b = max(done, seq_begin(a, s)), e = max(b, seq_begin(a, s + 1));
+    if (a.dscores)
+      for (int t = done + wave; t < b; t += SMALL_WAVES) zero_row<VEC, NV>(a, t, lane);
+    done = e;
+    for (int i = tid; i <= a.n; i += 64 * SMALL_WAVES) hist[i] = 0;
+    __syncthreads();
+    count_range(a, b, e, hist, hist + a.n);
+    __syncthreads();
+    const int many = hist[a.n];
+    for (int i = tid; i < a.n; i += 64 * SMALL_WAVES)
+      a.counts[static_cast<int64_t>(s) * a.n + i] = hist[i];
+    float c[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = column<VEC>(i, lane);
+      c[i] = col < a.n ? static_cast<float>(hist[col]) : 0.f;
+    }
+    const float coef = coefficient(a, s, many);
+    float sum = 0.f;
+    for (int t = b + wave; t < e; t += SMALL_WAVES) {
+      if (a.mask && !a.mask[t]) {
+        if (a.dscores) zero_row<VEC, NV>(a, t, lane);
+        continue;
+      }
+      float v[NV];
+      load_row<VEC, NV>(a.scores + t * a.ld, a.n, lane, v);
+      sum += a.dscores ? token<VEC, NV, true>(a, t, v, c, coef, lane)
+                       : token<VEC, NV, false>(a, t, v, c, coef, lane);
+    }
+    if (lane == 0) red[wave] = sum;
+    __syncthreads();  // also: everyone is done with hist
+    if (tid == 0) {
+      double total = 0.0;
+      for (int w = 0; w < SMALL_WAVES; ++w) total += red[w];
+      a.tokens[s] = many;
+      a.loss[s] = many ? static_cast<float>(static_cast<double>(a.n) /
+                                            (static_cast<double>(a.k) * many * many) * total)
+                       : 0.f;
+    }
+  }
+  if (a.dscores)
+    for (int t = done + wave; t < a.T; t += SMALL_WAVES) zero_row<VEC, NV>(a, t, lane);
+}
+
 template <int VEC, int NV>
 static void launch_pass(const Args& a, int waves, hipStream_t st) {
   const dim3 grid((waves + WAVES - 1) / WAVES), block(64 * WAVES);
@@ -295,25 +351,39 @@ static void launch_pass(const Args& a, int waves, hipStream_t st) {
     hipLaunchKernelGGL((pass_k<VEC, NV, false, true>), grid, block, 0, st, a);
 }
 
-static int pass(const Args& a, hipStream_t st) {
-  const int waves = (a.T + a.rpw - 1) / a.rpw;
+template <int VEC, int NV>
+static void launch(const Args& a, bool small, hipStream_t st) {
+  if (small)
+    hipLaunchKernelGGL((small_k<VEC, NV>), dim3(1), dim3(64 * SMALL_WAVES), 0, st, a);
+  else
+    launch_pass<VEC, NV>(a, (a.T + a.rpw - 1) / a.rpw, st);
+}
+
+static int pass(const Args& a, bool small, hipStream_t st) {
   const bool vec = a.n % 4 == 0 && a.ld % 4 == 0 &&
                    reinterpret_cast<uintptr_t>(a.scores) % 16 == 0 &&
                    reinterpret_cast<uintptr_t>(a.dscores) % 16 == 0;
   if (vec) {
     if (a.n <= 256)
-      launch_pass<4, 4>(a, waves, st);
+      launch<4, 4>(a, small, st);
     else if (a.n <= 512)
-      launch_pass<4, 8>(a, waves, st);
+      launch<4, 8>(a, small, st);
     else
-      launch_pass<4, 16>(a, waves, st);
+      launch<4, 16>(a, small, st);
   } else if (a.n <= 256) {
-    launch_pass<1, 4>(a, waves, st);
+    launch<1, 4>(a, small, st);
   } else {
-    launch_pass<1, 16>(a, waves, st);
+    launch<1, 16>(a, small, st);
   }
   MOE_LAUNCH_CHECK();
   return MOE_OK;
+}
+
+// One block's work against three more launches: 64 x 896 takes 17 us a call here
+// and 25 in four launches, 256 x 256 in 4 sequences 21 against 25; with 1024
+// tokens (33) or 8 sequences (40 to 53) the one block is the slower.
+static bool is_small(int T, int n, int S) {
+  return T <= 256 && static_cast<int64_t>(T) * n <= 65536 && S <= 4;
 }
 
 // Tokens per wave: 16 waves on each of 256 compute units.
@@ -351,6 +421,7 @@ extern "C" int moe_balance_loss(const float* scores, int64_t ld_scores, int32_t 
          dloss,  counts,    tokens, loss, dscores, static_cast<float*>(workspace),
          rows_per_wave(T)};
   hipStream_t hs = static_cast<hipStream_t>(stream);
+  if (is_small(T, n, n_seq)) return pass(a, true, hs);
   const int64_t cells = static_cast<int64_t>(n_seq) * n;
   hipLaunchKernelGGL(clear_k, dim3(static_cast<unsigned>(std::min<int64_t>((cells + 255) / 256, 4096))),
                      dim3(256), 0, hs, a);
@@ -358,7 +429,7 @@ extern "C" int moe_balance_loss(const float* scores, int64_t ld_scores, int32_t 
     const int chunk = std::max(16, (T + 511) / 512);
     hipLaunchKernelGGL(count_k, dim3((T + chunk - 1) / chunk), dim3(256), 0, hs, a, chunk);
     MOE_LAUNCH_CHECK();
-    const int rc = pass(a, hs);
+    const int rc = pass(a, false, hs);
     if (rc != MOE_OK) return rc;
   }
   hipLaunchKernelGGL(finish_k, dim3(std::min(n_seq, 2048)), dim3(256), 0, hs, a);
@@ -380,5 +451,5 @@ extern "C" int moe_balance_loss_backward(const float* scores, int64_t ld_scores,
   Args a{scores, ld_scores, T, n, k, nullptr, seq_offsets, n_seq, token_mask, dloss,
          const_cast<int32_t*>(counts), const_cast<int32_t*>(tokens), nullptr, dscores, nullptr,
          rows_per_wave(T)};
-  return pass(a, static_cast<hipStream_t>(stream));
+  return pass(a, false, static_cast<hipStream_t>(stream));
 }

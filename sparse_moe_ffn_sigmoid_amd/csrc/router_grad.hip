@@ -91,20 +91,32 @@ __global__ __launch_bounds__(256) void score_grad_k(const float* __restrict__ sc
   }
 }
 
-// out[c][r] = in[r][c], zeros from R to ld_out; fp32 input in two parts.
+// out[c][r] = in[r][c], zeros from R to ld_out; fp32 input in two parts.  Tiles
+// of 128 rows x 64 columns: 16 bytes per lane in, 256 consecutive bytes of an
+// output row out.
+constexpr int TROWS = 128;
+
 template <typename IN>
 __global__ __launch_bounds__(256) void transpose_k(const IN* __restrict__ in, int R, int C,
                                                    int64_t ld_out, bf16_t* __restrict__ hi,
                                                    bf16_t* __restrict__ lo) {
-  __shared__ IN tile[TILE][TILE + 1];
-  const int c0 = blockIdx.x * TILE, r0 = blockIdx.y * TILE;
-  for (int i = threadIdx.x; i < TILE * TILE; i += 256) {
-    const int r = i / TILE, c = i % TILE;
-    tile[r][c] = r0 + r < R ? in[static_cast<int64_t>(r0 + r) * C + c0 + c] : IN(0);
+  constexpr int PER = 16 / sizeof(IN), LPR = TILE / PER;  // elements per load, lanes per row
+  __shared__ IN tile[TROWS][TILE + 1];
+  const int c0 = blockIdx.x * TILE, r0 = blockIdx.y * TROWS;
+#pragma unroll
+  for (int i = threadIdx.x; i < TROWS * LPR; i += 256) {
+    const int r = i / LPR, c = i % LPR * PER;
+    __attribute__((aligned(16))) IN v[PER] = {};
+    if (r0 + r < R)
+      *reinterpret_cast<uint4*>(v) =
+          *reinterpret_cast<const uint4*>(in + static_cast<int64_t>(r0 + r) * C + c0 + c);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) tile[r][c + j] = v[j];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < TILE * TILE / 8; i += 256) {
-    const int c = i / 8, r = i % 8 * 8;
+  for (int i = threadIdx.x; i < TILE * TROWS / 8; i += 256) {
+    const int c = i / (TROWS / 8), r = i % (TROWS / 8) * 8;
+    if (r0 + r >= ld_out) continue;
     const int64_t at = (c0 + c) * ld_out + r0 + r;
     bf16_t h[8], l[8];
     if constexpr (std::is_same<IN, float>::value) {
@@ -117,6 +129,62 @@ __global__ __launch_bounds__(256) void transpose_k(const IN* __restrict__ in, in
     }
     store8(hi + at, h);
   }
+}
+
+// A small layer in one launch, in fp32: a block takes CW columns of x, dx, W_r
+// and dW_r with all of g in LDS.
+constexpr int CW = 16;
+
+__global__ __launch_bounds__(256) void small_k(const bf16_t* __restrict__ x,
+                                               const float* __restrict__ w,
+                                               const float* __restrict__ scores,
+                                               const float* __restrict__ dscores, int T, int d,
+                                               int n, int accumulate, bf16_t* __restrict__ dx,
+                                               float* __restrict__ dw, float* __restrict__ doff) {
+  extern __shared__ float lds[];
+  float* const g = lds;           // [T][n]
+  float* const wc = g + T * n;    // [n][CW]
+  float* const xc = wc + n * CW;  // [T][CW]
+  const int c0 = blockIdx.x * CW, tid = threadIdx.x;
+  for (int i = tid; i < T * n; i += 256) {
+    const float s = scores[i];
+    g[i] = dscores[i] * (s * (1.f - s));
+  }
+  if (dx)
+    for (int i = tid; i < n * CW; i += 256) wc[i] = w[static_cast<int64_t>(i / CW) * d + c0 + i % CW];
+  if (dw)
+    for (int i = tid; i < T * CW; i += 256)
+      xc[i] = bf16_to_f32(x[static_cast<int64_t>(i / CW) * d + c0 + i % CW]);
+  __syncthreads();
+  if (dx)
+    for (int i = tid; i < T * CW; i += 256) {
+      const int t = i / CW, c = i % CW;
+      float sum = 0.f;
+#pragma unroll 8
+      for (int e = 0; e < n; ++e) sum = fmaf(g[t * n + e], wc[e * CW + c], sum);
+      bf16_t* const o = dx + static_cast<int64_t>(t) * d + c0 + c;
+      *o = f32_to_bf16(accumulate ? bf16_to_f32(*o) + sum : sum);
+    }
+  if (dw)
+    for (int i = tid; i < n * CW; i += 256) {
+      const int e = i / CW, c = i % CW;
+      float sum = 0.f;
+#pragma unroll 8
+      for (int t = 0; t < T; ++t) sum = fmaf(g[t * n + e], xc[t * CW + c], sum);
+      float* const o = dw + static_cast<int64_t>(e) * d + c0 + c;
+      *o = accumulate ? *o + sum : sum;
+    }
+  if (doff && blockIdx.x == 0)
+    for (int e = tid; e < n; e += 256) {
+      double sum = 0.0;
+      for (int t = 0; t < T; ++t) sum += g[t * n + e];
+      const float v = static_cast<float>(sum);
+      doff[e] = accumulate ? doff[e] + v : v;
+    }
+}
+
+static size_t small_bytes(int T, int n) {
+  return 4 * (static_cast<size_t>(T) * n + static_cast<size_t>(T + n) * CW);
 }
 
 // d_offset from the tiles' sums, in 64 bits and a fixed order
@@ -175,6 +243,12 @@ static size_t layout(int T, int d, int n, Workspace* out, void* base) {
   return cv.bytes();
 }
 
+// What one launch of fp32 multiply-adds does sooner than seven: LDS for g, and
+// little enough work per column.
+static bool is_small(int T, int d, int n) {
+  return small_bytes(T, n) <= 96 * 1024 && static_cast<int64_t>(T) * n * d <= (8 << 20);
+}
+
 static int check(int32_t T, int32_t d, int32_t n) {
   if (T < 0 || d <= 0 || d % 64 || n < 1) return MOE_EINVAL;
   if (n > 1024 || T > MOE_MAX_TOKENS || d > (1 << 20)) return MOE_EUNSUPPORTED;
@@ -220,7 +294,9 @@ extern "C" int moe_router_backward(const void* x, const float* w_router, const f
   if (T > 0 && (!scores || !dscores || (dx && !w_router) || (d_w_router && !x)))
     return MOE_EINVAL;
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MOE_EINVAL;
-  if (reinterpret_cast<uintptr_t>(dx) % 16 != 0 || reinterpret_cast<uintptr_t>(d_w_router) % 16 != 0)
+  if (reinterpret_cast<uintptr_t>(x) % 16 != 0 || reinterpret_cast<uintptr_t>(w_router) % 16 != 0 ||
+      reinterpret_cast<uintptr_t>(dx) % 16 != 0 ||
+      reinterpret_cast<uintptr_t>(d_w_router) % 16 != 0)
     return MOE_EINVAL;
   Workspace w;
   if (workspace_bytes < layout(T, d, n, &w, workspace)) return MOE_EWORKSPACE;
@@ -237,6 +313,13 @@ extern "C" int moe_router_backward(const void* x, const float* w_router, const f
     MOE_LAUNCH_CHECK();
     return MOE_OK;
   }
+  if (is_small(T, d, n)) {
+    hipLaunchKernelGGL(small_k, dim3(d / CW), dim3(256), small_bytes(T, n), st,
+                       static_cast<const bf16_t*>(x), w_router, scores, dscores, T, d, n,
+                       accumulate, static_cast<bf16_t*>(dx), d_w_router, d_router_logit_offset);
+    MOE_LAUNCH_CHECK();
+    return MOE_OK;
+  }
   const unsigned tn = static_cast<unsigned>(np / 64), tt = static_cast<unsigned>(Tp / 64),
                  td = static_cast<unsigned>(d / 64);
   hipLaunchKernelGGL(score_grad_k, dim3(tn, tt), dim3(256), 0, st, scores, dscores, T, n, np, Tp,
@@ -248,7 +331,7 @@ extern "C" int moe_router_backward(const void* x, const float* w_router, const f
     MOE_LAUNCH_CHECK();
   }
   if (d_w_router) {
-    hipLaunchKernelGGL(transpose_k<bf16_t>, dim3(td, tt), dim3(256), 0, st,
+    hipLaunchKernelGGL(transpose_k<bf16_t>, dim3(td, (tt + 1) / 2), dim3(256), 0, st,
                        static_cast<const bf16_t*>(x), T, d, Tp, w.xt, nullptr);
     MOE_LAUNCH_CHECK();
     rc = product3(w, {w.gt_hi, w.gt_mid, w.gt_lo}, {w.xt, w.xt, w.xt}, Tp, n, d,
@@ -260,7 +343,7 @@ extern "C" int moe_router_backward(const void* x, const float* w_router, const f
     }
   }
   if (dx) {
-    hipLaunchKernelGGL(transpose_k<float>, dim3(td, tn), dim3(256), 0, st, w_router, n, d, np,
+    hipLaunchKernelGGL(transpose_k<float>, dim3(td, (tn + 1) / 2), dim3(256), 0, st, w_router, n, d, np,
                        w.wt_hi, w.wt_lo);
     MOE_LAUNCH_CHECK();
     rc = product3(w, {w.g_hi, w.g_hi, w.g_lo}, {w.wt_hi, w.wt_lo, w.wt_hi}, np, T, d,
