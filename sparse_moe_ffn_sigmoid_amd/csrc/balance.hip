@@ -106,7 +106,9 @@ __device__ __forceinline__ void count_range(const Args& a, int b, int e, int32_t
 
 // Counts per sequence: a histogram in LDS for each stretch of a block's tokens
 // that lies in one sequence, added to global memory.
-__global__ __launch_bounds__(256) void count_k(Args a, int chunk) {
+constexpr int COUNT_THREADS = 1024;
+
+__global__ __launch_bounds__(COUNT_THREADS) void count_k(Args a, int chunk) {
   __shared__ int32_t hist[MAXN + 1];
   int t = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(blockIdx.x) * chunk, a.T));
   const int end = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(t) + chunk, a.T));
@@ -114,11 +116,11 @@ __global__ __launch_bounds__(256) void count_k(Args a, int chunk) {
     t = max(t, seq_begin(a, s));
     const int e = min(end, seq_begin(a, s + 1));
     if (e <= t) continue;
-    for (int i = threadIdx.x; i <= a.n; i += 256) hist[i] = 0;
+    for (int i = threadIdx.x; i <= a.n; i += COUNT_THREADS) hist[i] = 0;
     __syncthreads();
     count_range(a, t, e, hist, hist + a.n);
     __syncthreads();
-    for (int i = threadIdx.x; i < a.n; i += 256)
+    for (int i = threadIdx.x; i < a.n; i += COUNT_THREADS)
       if (hist[i]) atomicAdd(a.counts + static_cast<int64_t>(s) * a.n + i, hist[i]);
     if (threadIdx.x == 0 && hist[a.n]) atomicAdd(a.tokens + s, hist[a.n]);
     __syncthreads();
@@ -426,8 +428,9 @@ extern "C" int moe_balance_loss(const float* scores, int64_t ld_scores, int32_t 
   hipLaunchKernelGGL(clear_k, dim3(static_cast<unsigned>(std::min<int64_t>((cells + 255) / 256, 4096))),
                      dim3(256), 0, hs, a);
   if (T > 0) {
-    const int chunk = std::max(16, (T + 511) / 512);
-    hipLaunchKernelGGL(count_k, dim3((T + chunk - 1) / chunk), dim3(256), 0, hs, a, chunk);
+    // few blocks: each adds up to n counts per sequence to global memory
+    const int chunk = std::max(64, (T + 127) / 128);
+    hipLaunchKernelGGL(count_k, dim3((T + chunk - 1) / chunk), dim3(COUNT_THREADS), 0, hs, a, chunk);
     MOE_LAUNCH_CHECK();
     const int rc = pass(a, false, hs);
     if (rc != MOE_OK) return rc;

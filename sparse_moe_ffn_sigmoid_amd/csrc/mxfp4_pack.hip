@@ -63,20 +63,22 @@ __global__ __launch_bounds__(256) void pack_rows_k(PackArgs a) {
   }
 }
 
-// Columns, with or without rows: a block takes 128 rows (four blocks of 32 of
+// Columns, with or without rows: a block takes 256 rows (eight blocks of 32 of
 // each column) by TC columns.  The rows come in as in pack_rows_k, are packed
 // from registers if wanted and laid down in LDS; then each thread packs the 32
-// rows of one block for each of its columns.  The LDS words of the four row
-// blocks are turned by 16 words against each other, so that 16 columns by four
-// row blocks, one wave's read, hit 64 different banks, and four neighbouring
-// lanes write 64 consecutive bytes of a column.
+// rows of one block for each of its columns.  The LDS words of the row blocks
+// are turned by 8 words against each other, so that 8 columns by eight row
+// blocks, one wave's read, hit 64 different banks, and eight neighbouring lanes
+// write 128 consecutive bytes of a column.
+constexpr int PACK_ROWS = 256;  // rows of a tile, half its threads
+
 template <int DT, bool WITH_ROWS>
-__global__ __launch_bounds__(256) void pack_cols_k(PackArgs a) {
+__global__ __launch_bounds__(2 * PACK_ROWS) void pack_cols_k(PackArgs a) {
   typedef typename Elem<DT>::type E;
   constexpr int PER = 4 / sizeof(E);  // elements per LDS word
-  constexpr int TR = 128, TC = 64 * PER;
+  constexpr int TR = PACK_ROWS, NTH = 2 * TR, TC = 64 * PER;
   constexpr int LPR = TC / 8;          // lanes per row while loading
-  constexpr int RPP = 256 / LPR;       // rows per step
+  constexpr int RPP = NTH / LPR;       // rows per step
   __shared__ uint32_t tile[TR * 64];
   __shared__ int32_t src[TR];          // input row of each row of the tile, -1: none
   const int tid = threadIdx.x;
@@ -136,16 +138,16 @@ __global__ __launch_bounds__(256) void pack_cols_k(PackArgs a) {
         const f16x2_t h = {static_cast<_Float16>(v[2 * w]), static_cast<_Float16>(v[2 * w + 1])};
         __builtin_memcpy(&bits, &h, 4);
       }
-      tile[r * 64 + ((w0 + w + 16 * (r >> 5)) & 63)] = bits;
+      tile[r * 64 + ((w0 + w + 8 * (r >> 5)) & 63)] = bits;
     }
   }
   __syncthreads();
-  const int rb = tid & 3, word = tid >> 2;
+  const int rb = tid % (TR / 32), word = tid / (TR / 32);
   const int64_t blk = (p0 >> 5) + rb;
   if (blk >= a.rb || (a.off && p0 + rb * 32 >= a.poff[a.G])) return;
   uint32_t raw[32];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) raw[i] = tile[(rb * 32 + i) * 64 + ((word + 16 * rb) & 63)];
+  for (int i = 0; i < 32; ++i) raw[i] = tile[(rb * 32 + i) * 64 + ((word + 8 * rb) & 63)];
 #pragma unroll
   for (int h = 0; h < PER; ++h) {
     const int64_t col = c0 + word * PER + h;
@@ -200,6 +202,21 @@ __global__ __launch_bounds__(1024) void pad_groups_k(const int32_t* __restrict__
   if (g < G) poff[g + 1] = static_cast<int32_t>(min(sum, room));
 }
 
+// Codes 2 j and 2 j + 1 of a word times the scale, in the output's type.
+template <int DT, int J>
+__device__ __forceinline__ auto decode2(uint32_t q, float scale) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if constexpr (DT == MOE_F32)
+    return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, scale, J);
+  else if constexpr (DT == MOE_BF16)
+    return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, J);
+  else
+    return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, scale, J);
+#else
+  return 0;
+#endif
+}
+
 // Codes back to values: a wave takes 512 elements of a row, 8 per lane.
 template <int DT>
 __global__ __launch_bounds__(256) void unpack_k(const uint8_t* __restrict__ codes,
@@ -224,20 +241,22 @@ __global__ __launch_bounds__(256) void unpack_k(const uint8_t* __restrict__ code
 #pragma unroll
     for (int i = 0; i < ROWS_PER; ++i) {
       if (r0 + i >= rows) break;
-      // E2M1 magnitude m is 0, 1/2, then (2 + (m & 1)) 2^(m/2 - 2); the product
-      // with 2^(s - 127) is exact in fp32 (two significant bits, at least 2^-128)
-      const float sc = s[i] == 255u ? __uint_as_float(0x7fc00000u) : scale_value(s[i]);
+      // the hardware conversion takes the scale's exponent field as it is: 2^-127
+      // at 0, NaN at 255
+      const float sc = __uint_as_float(s[i] << 23);
       __attribute__((aligned(16))) E e[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t nib = (q[i] >> (4 * j)) & 15u, m = nib & 7u;
-        const uint32_t bits = m < 2u ? (m ? 0x3f000000u : 0u) : ((126u + (m >> 1)) << 23) | ((m & 1u) << 22);
-        const float f = __uint_as_float(bits | ((nib & 8u) << 28)) * sc;
-        if constexpr (DT == MOE_BF16)
-          e[j] = f32_to_bf16(f);
-        else
-          e[j] = static_cast<E>(f);
-      }
+#if defined(__HIP_DEVICE_COMPILE__)
+#define MOE_UNPACK2(j)                                                          \
+  {                                                                             \
+    const auto v = decode2<DT, j>(q[i], sc);                                    \
+    __builtin_memcpy(e + 2 * (j), &v, 2 * sizeof(E));                           \
+  }
+      MOE_UNPACK2(0)
+      MOE_UNPACK2(1)
+      MOE_UNPACK2(2)
+      MOE_UNPACK2(3)
+#undef MOE_UNPACK2
+#endif
       E* dst = out + (r0 + i) * row_stride;
       if (vec && c + 8 <= cols) {
 #pragma unroll
@@ -266,11 +285,12 @@ static void launch_pack(const PackArgs& a, int64_t batch, hipStream_t st) {
   }
   constexpr int TC = DT == MOE_F32 ? 64 : 128;
   const dim3 grid(static_cast<unsigned>((a.cols + TC - 1) / TC),
-                  static_cast<unsigned>((a.rb + 3) / 4), static_cast<unsigned>(batch));
+                  static_cast<unsigned>((a.rb * 32 + PACK_ROWS - 1) / PACK_ROWS),
+                  static_cast<unsigned>(batch));
   if (a.codes)
-    hipLaunchKernelGGL((pack_cols_k<DT, true>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((pack_cols_k<DT, true>), grid, dim3(2 * PACK_ROWS), 0, st, a);
   else
-    hipLaunchKernelGGL((pack_cols_k<DT, false>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((pack_cols_k<DT, false>), grid, dim3(2 * PACK_ROWS), 0, st, a);
 }
 
 }  // namespace mx

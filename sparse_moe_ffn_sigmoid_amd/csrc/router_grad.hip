@@ -135,29 +135,41 @@ __global__ __launch_bounds__(256) void transpose_k(const IN* __restrict__ in, in
 // and dW_r with all of g in LDS.
 constexpr int CW = 16;
 
-__global__ __launch_bounds__(256) void small_k(const bf16_t* __restrict__ x,
-                                               const float* __restrict__ w,
-                                               const float* __restrict__ scores,
-                                               const float* __restrict__ dscores, int T, int d,
-                                               int n, int accumulate, bf16_t* __restrict__ dx,
-                                               float* __restrict__ dw, float* __restrict__ doff) {
+constexpr int SMALL_THREADS = 1024;
+
+__global__ __launch_bounds__(SMALL_THREADS) void small_k(
+    const bf16_t* __restrict__ x, const float* __restrict__ w, const float* __restrict__ scores,
+    const float* __restrict__ dscores, int T, int d, int n, int accumulate,
+    bf16_t* __restrict__ dx, float* __restrict__ dw, float* __restrict__ doff) {
   extern __shared__ float lds[];
   float* const g = lds;           // [T][n]
   float* const wc = g + T * n;    // [n][CW]
   float* const xc = wc + n * CW;  // [T][CW]
   const int c0 = blockIdx.x * CW, tid = threadIdx.x;
-  for (int i = tid; i < T * n; i += 256) {
+  for (int i = tid; i < T * n; i += SMALL_THREADS) {
     const float s = scores[i];
     g[i] = dscores[i] * (s * (1.f - s));
   }
+  if (c0 >= d) {  // the block behind the columns adds up the offset's gradient
+    __syncthreads();
+    for (int e = tid >> 6; e < n; e += SMALL_THREADS / 64) {
+      double sum = 0.0;
+      for (int t = tid & 63; t < T; t += 64) sum += g[t * n + e];
+      for (int k = 32; k; k >>= 1) sum += __shfl_xor(sum, k);
+      const float v = static_cast<float>(sum);
+      if ((tid & 63) == 0) doff[e] = accumulate ? doff[e] + v : v;
+    }
+    return;
+  }
   if (dx)
-    for (int i = tid; i < n * CW; i += 256) wc[i] = w[static_cast<int64_t>(i / CW) * d + c0 + i % CW];
+    for (int i = tid; i < n * CW; i += SMALL_THREADS)
+      wc[i] = w[static_cast<int64_t>(i / CW) * d + c0 + i % CW];
   if (dw)
-    for (int i = tid; i < T * CW; i += 256)
+    for (int i = tid; i < T * CW; i += SMALL_THREADS)
       xc[i] = bf16_to_f32(x[static_cast<int64_t>(i / CW) * d + c0 + i % CW]);
   __syncthreads();
   if (dx)
-    for (int i = tid; i < T * CW; i += 256) {
+    for (int i = tid; i < T * CW; i += SMALL_THREADS) {
       const int t = i / CW, c = i % CW;
       float sum = 0.f;
 #pragma unroll 8
@@ -166,20 +178,13 @@ __global__ __launch_bounds__(256) void small_k(const bf16_t* __restrict__ x,
       *o = f32_to_bf16(accumulate ? bf16_to_f32(*o) + sum : sum);
     }
   if (dw)
-    for (int i = tid; i < n * CW; i += 256) {
+    for (int i = tid; i < n * CW; i += SMALL_THREADS) {
       const int e = i / CW, c = i % CW;
       float sum = 0.f;
 #pragma unroll 8
       for (int t = 0; t < T; ++t) sum = fmaf(g[t * n + e], xc[t * CW + c], sum);
       float* const o = dw + static_cast<int64_t>(e) * d + c0 + c;
       *o = accumulate ? *o + sum : sum;
-    }
-  if (doff && blockIdx.x == 0)
-    for (int e = tid; e < n; e += 256) {
-      double sum = 0.0;
-      for (int t = 0; t < T; ++t) sum += g[t * n + e];
-      const float v = static_cast<float>(sum);
-      doff[e] = accumulate ? doff[e] + v : v;
     }
 }
 
@@ -314,7 +319,8 @@ extern "C" int moe_router_backward(const void* x, const float* w_router, const f
     return MOE_OK;
   }
   if (is_small(T, d, n)) {
-    hipLaunchKernelGGL(small_k, dim3(d / CW), dim3(256), small_bytes(T, n), st,
+    hipLaunchKernelGGL(small_k, dim3(d / CW + (d_router_logit_offset ? 1 : 0)),
+                       dim3(SMALL_THREADS), small_bytes(T, n), st,
                        static_cast<const bf16_t*>(x), w_router, scores, dscores, T, d, n,
                        accumulate, static_cast<bf16_t*>(dx), d_w_router, d_router_logit_offset);
     MOE_LAUNCH_CHECK();

@@ -196,7 +196,7 @@ def test_matmul(M, N, K):
 @pytest.mark.parametrize("dtype", [BF16, F32, F16])
 def test_linear(M, dtype):
     import sparse_moe_ffn_sigmoid_amd as moe
-    for N, K in ((100, 64), (3, 32), (500, 1184), (64, 4096)):
+    for N, K in ((100, 64), (3, 32), (500, 1184), (64, 4096), (20, 7168), (33, 8224)):
         announce(f"linear {dtype} {M}x{N}x{K}")
         x, w = operand(M, K, M + N, dtype), operand(N, K, N, F32)
         p = moe.mxfp4_pack(w.cuda())
