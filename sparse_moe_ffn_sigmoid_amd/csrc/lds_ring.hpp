@@ -60,4 +60,10 @@ __device__ __forceinline__ void ring_wait() {
   asm volatile("" ::: "memory");
 }
 
+// Wait for this wave's LDS accesses.
+__device__ __forceinline__ void lds_wait() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  asm volatile("" ::: "memory");
+}
+
 }  // namespace moe

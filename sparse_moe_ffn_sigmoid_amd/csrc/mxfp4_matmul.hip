@@ -402,6 +402,7 @@ struct Ring {
   template <int NF>
   static __device__ __forceinline__ void products(const Tile& t, Cursor& cur, int& buf, Shared& sh,
                                                   f32x16_t (&acc)[NF][FN]) {
+    const bool copies = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) < LW;
     constexpr int SR = BN + NF * WM * 32;  // scale rows that are used
 #pragma unroll
     for (int i = 0; i < NF; ++i)
@@ -411,8 +412,9 @@ struct Ring {
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
     bool second = false;  // of the pair of buffers whose scales were loaded
     for (int kb = t.kb0; kb < t.kb1; kb += 8) {
-      ring_wait<0>();   // this wave's copies of the buffer to be used
-      __syncthreads();  // everyone's; and everyone is done with the other buffer
+      if (copies) ring_wait<0>();  // this wave's copies of the buffer to be used
+      lds_wait();
+      ring_barrier();  // everyone's; and everyone is done with the other buffer
       if (kb + 8 < t.kb1) {
         put_scales(cur, !second, buf ^ 1, SR, sh);
         if (!second && kb + 16 < t.kb1) load_scales(cur, t, kb + 16, SR);
@@ -818,13 +820,16 @@ static int skinny(const MatArgs& a, int64_t per_group, hipStream_t st) {
   return waves >= 8192 ? launch_skinny<4, 1, 1, 1, 4>(a, st) : launch_skinny<1, 8, 1, 1, 4>(a, st);
 }
 
-// Rows per problem up to which the codes of B bound the time and the skinny
-// kernel is taken.
-constexpr int SKINNY_ROWS = 32;
+// Rows per problem up to which the skinny kernel is the faster.  One problem, K =
+// 7168: 64 rows 14.7 us against the ring kernel's 25.5 at N = 3584 and 26.6
+// against 28.5 at N = 7168; 128 rows 27.4 against 25.9 and 50.5 against 28.9.  64
+// groups of 2048 x 3584: past 16 rows each it reads the weights' codes once more
+// per 64 rows without the others' sharing them, 17 rows 75.9 us against 45.1.
+constexpr int SKINNY_ROWS = 64, SKINNY_GROUP_ROWS = 16;
 
 // Tile height: the multiple of 64 up to 320 whose tiles cover the rows of a
-// problem with the least work per compute unit, the taller one on a tie (fewer
-// reads of B).
+// problem soonest, a tile of h rows costing h and the 128 rows' worth that every
+// tile's weights and start take; the taller one on a tie (fewer reads of B).
 static int tile_height(int64_t rows, int64_t problems, int64_t N) {
   int best = 64;
   int64_t cost = 0;
@@ -852,7 +857,7 @@ static int product(const MatArgs& a, hipStream_t st) {
     return ring_fits(a) ? launch_ring<2, 4, 5, 2>(a, tile_height(a.M, a.G, a.N), st)
                         : MOE_EUNSUPPORTED;
   const int64_t per = a.off ? (a.M + a.G - 1) / a.G : a.M;
-  if (per <= SKINNY_ROWS || !ring_fits(a)) return skinny(a, per, st);
+  if (per <= (a.off ? SKINNY_GROUP_ROWS : SKINNY_ROWS) || !ring_fits(a)) return skinny(a, per, st);
   return launch_ring<2, 4, 5, 2>(a, tile_height(per, a.off ? a.G : 1, a.N), st);
 }
 
