@@ -443,7 +443,8 @@ int moe_balance_loss_backward(const float* scores, int64_t ld_scores, int32_t T,
  * (moe_latent_backward's own gradient reaches the router through the chosen
  * scores only; a loss on all scores, as the balance loss, comes in here.)
  *   x [T][d] bf16, w_router [n][d] f32, scores and dscores [T][n] f32
- *            (contiguous); d a multiple of 64, n <= 1024
+ *            (contiguous); d a multiple of 64, n <= 1024; x, w_router, dx and
+ *            d_w_router 16-byte aligned
  *   accumulate 0: outputs are overwritten; 1: added to (dx = bf16(dx + .),
  *            the others in fp32), for gradients moe_latent_backward wrote
  *   dx [T][d] bf16, d_w_router [n][d] f32, d_router_logit_offset [n] f32;
@@ -511,9 +512,11 @@ int moe_mxfp4_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, 
  *   row_offsets NULL (n_groups = 1): one product of M rows.  Else [n_groups + 1]
  *            i32, non-decreasing, n_groups <= 1024: rows [row_offsets[g],
  *            row_offsets[g + 1]) of C meet matrix g.  Rows of C outside every
- *            group are left as they were
- *   row_index [M] i32 or NULL: row r of C is made from row row_index[r] of A
- *            (an index outside [0, a_rows) makes it a row of zeros); NULL: row r
+ *            group are left as they were.  At most 2^24 rows with groups, 2^30
+ *            without
+ *   row_index [M] i32 or NULL: row r of C is made from row row_index[r] of A,
+ *            a_rows >= 1 (an index outside [0, a_rows) makes it a row of
+ *            zeros); NULL: row r
  *   out      [M][N] of out_dtype (MOE_F32, MOE_BF16, MOE_F16), rows ld_out
  *            elements apart, rounded once from the fp32 sum
  */

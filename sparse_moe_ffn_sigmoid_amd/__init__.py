@@ -426,12 +426,12 @@ def _mx_type(dtype, name):
 def _mx_operand(codes, scales, name, dim, dev):
     """Shape [.., rows, K] of packed codes [.., rows, K/2] and their scales."""
     if not isinstance(codes, torch.Tensor) or codes.dim() != dim:
-        raise ValueError(f"{name}_codes must be a tensor of {dim} dimensions")
+        raise ValueError(f"{name}codes must be a tensor of {dim} dimensions")
     shape = tuple(codes.shape)
     if shape[-1] == 0 or shape[-1] % 16:
-        raise ValueError(f"{name}_codes must hold whole blocks of 32 elements (16 bytes)")
-    _check(codes, f"{name}_codes", torch.uint8, shape, dev)
-    _check(scales, f"{name}_scales", torch.uint8, shape[:-1] + (shape[-1] // 16,), dev)
+        raise ValueError(f"{name}codes must hold whole blocks of 32 elements (16 bytes)")
+    _check(codes, f"{name}codes", torch.uint8, shape, dev)
+    _check(scales, f"{name}scales", torch.uint8, shape[:-1] + (shape[-1] // 16,), dev)
     return shape[:-1] + (2 * shape[-1],)
 
 
@@ -531,9 +531,9 @@ def mxfp4_matmul(a_codes, a_scales, b_codes, b_scales, offsets=None, rows=None,
     C is made from row rows[r] of A, M = R without it.
     """
     dev = _device_of(a_codes, "a_codes")
-    R, K = _mx_operand(a_codes, a_scales, "a", 2, dev)
+    R, K = _mx_operand(a_codes, a_scales, "a_", 2, dev)
     G = _groups(offsets, b_codes.dim(), dev)
-    b = _mx_operand(b_codes, b_scales, "b", 2 if offsets is None else 3, dev)
+    b = _mx_operand(b_codes, b_scales, "b_", 2 if offsets is None else 3, dev)
     if b[-1] != K or (offsets is not None and b[0] != G):
         raise ValueError(f"b is {b}: K = {K} and {G} groups are wanted")
     M, N = R, b[-2]
@@ -555,8 +555,8 @@ def mxfp4_matmul_kgroup(a_codes, a_scales, b_codes, b_scales, offsets=None,
     from ``offsets`` (its offsets_t).  Returns [G, M, N], or [M, N] over all of
     K without ``offsets``."""
     dev = _device_of(a_codes, "a_codes")
-    M, K = _mx_operand(a_codes, a_scales, "a", 2, dev)
-    N, Kb = _mx_operand(b_codes, b_scales, "b", 2, dev)
+    M, K = _mx_operand(a_codes, a_scales, "a_", 2, dev)
+    N, Kb = _mx_operand(b_codes, b_scales, "b_", 2, dev)
     if Kb != K:
         raise ValueError(f"the operands' K differ: {K} and {Kb}")
     dt = _mx_type(out_dtype, "out_dtype")
@@ -584,7 +584,7 @@ def mxfp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
     if x.stride(1) != 1 and K > 1 or rs < K:
         raise ValueError("x must have unit column stride and rows that do not overlap")
     G = _groups(offsets, w_codes.dim(), dev)
-    w = _mx_operand(w_codes, w_scales, "w", 2 if offsets is None else 3, dev)
+    w = _mx_operand(w_codes, w_scales, "w_", 2 if offsets is None else 3, dev)
     if w[-1] != K or (offsets is not None and w[0] != G):
         raise ValueError(f"the weights are {w}: K = {K} and {G} groups are wanted")
     M, N = R, w[-2]

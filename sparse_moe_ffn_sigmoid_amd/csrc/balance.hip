@@ -93,8 +93,8 @@ __global__ __launch_bounds__(256) void clear_k(Args a) {
 // hist and *many by the block's threads.
 __device__ __forceinline__ void count_range(const Args& a, int b, int e, int32_t* hist,
                                             int32_t* many) {
-  const int64_t last = static_cast<int64_t>(e) * a.k;
-  for (int64_t i = static_cast<int64_t>(b) * a.k + threadIdx.x; i < last; i += blockDim.x) {
+  const int last = e * a.k;  // at most 2^30
+  for (int i = b * a.k + static_cast<int>(threadIdx.x); i < last; i += blockDim.x) {
     if (a.mask && !a.mask[i / a.k]) continue;
     const int v = a.idx[i];
     if (v >= 0 && v < a.n) atomicAdd(hist + v, 1);  // indices outside the experts count nowhere

@@ -70,24 +70,40 @@ __device__ __forceinline__ uint32_t encode8(const float (&v)[8], uint32_t sb) {
   return w;
 }
 
-// 8 elements of a row, zeros behind `left` of them; one or two 16-byte loads
-// where the row allows it.
+// The bits of 8 elements of a row, zeros behind `left` of them; one or two
+// 16-byte loads where the row allows it.
+template <int DT>
+struct Raw8 {
+  typedef typename Elem<DT>::type E;
+  __attribute__((aligned(16))) uint32_t w[2 * sizeof(E)];
+
+  __device__ __forceinline__ void load(const E* p, int64_t left, bool vec) {
+    typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+    if (vec && left >= 8) {
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(E)) / 2; ++i)
+        *reinterpret_cast<u32x4_t*>(w + 4 * i) = reinterpret_cast<const u32x4_t*>(p)[i];
+    } else {
+      E e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = i < left ? p[i] : E(0);
+      __builtin_memcpy(w, e, sizeof(w));
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    E e[8];
+    __builtin_memcpy(e, w, sizeof(w));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = Elem<DT>::f32(e[i]);
+  }
+};
+
 template <int DT>
 __device__ __forceinline__ void load8(const typename Elem<DT>::type* p, int64_t left, bool vec,
                                       float (&v)[8]) {
-  typedef typename Elem<DT>::type E;
-  if (vec && left >= 8) {
-    typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-    __attribute__((aligned(16))) E e[8];
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(8 * sizeof(E)) / 16; ++i)
-      reinterpret_cast<u32x4_t*>(e)[i] = reinterpret_cast<const u32x4_t*>(p)[i];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = Elem<DT>::f32(e[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < left ? Elem<DT>::f32(p[i]) : 0.f;
-  }
+  Raw8<DT> raw;
+  raw.load(p, left, vec);
+  raw.values(v);
 }
 
 __device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {

@@ -505,6 +505,8 @@ __global__ __launch_bounds__(64 * WM * WN) void ring_k(MatArgs a, int h, int ntm
     R::count_tiles(a, h, sh);
     ntm = __builtin_amdgcn_readfirstlane(sh.first[a.G]);
   }
+  // offsets that fall could name more tiles than the launch allowed for
+  if (static_cast<int64_t>(ntm) * ntn * (a.kofs ? a.G : 1) > 0x7fff0000) return;
   const int tiles = ntm * ntn * (a.kofs ? a.G : 1);
   const int per = (tiles + 7) >> 3, step = gridDim.x >> 3;
   const int last = min(tiles, static_cast<int>(blockIdx.x & 7) * per + per);
@@ -861,6 +863,9 @@ static int product(const MatArgs& a, hipStream_t st) {
   return launch_ring<2, 4, 5, 2>(a, tile_height(per, a.off ? a.G : 1, a.N), st);
 }
 
+// Rows of C: tile counts of any row offsets stay within 32 bits.
+constexpr int64_t MAX_ROWS = 1 << 30, MAX_GROUPED_ROWS = 1 << 24;
+
 static bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 static int check_out(int32_t out_dtype, const void* out, int64_t ldo, int64_t N) {
@@ -883,8 +888,8 @@ extern "C" int moe_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales,
   using namespace moe::mx;
   if (M < 0 || N < 1 || K < 32 || K % 32 || a_rows < 0) return MOE_EINVAL;
   if (row_offsets ? n_groups < 1 : n_groups != 1) return MOE_EINVAL;
-  if (!row_index && a_rows < M) return MOE_EINVAL;
-  if (M > (1 << 30) || N > (1 << 30) || a_rows > (1 << 30) || K > (1 << 30) || n_groups > 1024)
+  if (row_index ? M > 0 && a_rows < 1 : a_rows < M) return MOE_EINVAL;
+  if (M > (row_offsets ? MAX_GROUPED_ROWS : MAX_ROWS) || N > (1 << 30) || a_rows > (1 << 30) || K > (1 << 30) || n_groups > 1024)
     return MOE_EUNSUPPORTED;
   if (M == 0) return MOE_OK;
   const int rc = check_out(out_dtype, out, ld_out, N);
@@ -961,9 +966,9 @@ extern "C" int moe_mxfp4_linear(const void* x, int32_t x_dtype, int64_t x_rows,
   using namespace moe::mx;
   if (M < 0 || N < 1 || K < 32 || K % 32 || x_rows < 0 || row_stride < K) return MOE_EINVAL;
   if (row_offsets ? n_groups < 1 : n_groups != 1) return MOE_EINVAL;
-  if (!row_index && x_rows < M) return MOE_EINVAL;
+  if (row_index ? M > 0 && x_rows < 1 : x_rows < M) return MOE_EINVAL;
   if (x_dtype != MOE_F32 && x_dtype != MOE_BF16 && x_dtype != MOE_F16) return MOE_EUNSUPPORTED;
-  if (M > (1 << 30) || N > (1 << 30) || x_rows > (1 << 30) || K > (1 << 30) || n_groups > 1024)
+  if (M > (row_offsets ? MAX_GROUPED_ROWS : MAX_ROWS) || N > (1 << 30) || x_rows > (1 << 30) || K > (1 << 30) || n_groups > 1024)
     return MOE_EUNSUPPORTED;
   if (row_stride > (int64_t(1) << 56) / (x_rows + 1)) return MOE_EINVAL;
   if (M == 0) return MOE_OK;

@@ -111,13 +111,23 @@ __global__ __launch_bounds__(2 * PACK_ROWS) void pack_cols_k(PackArgs a) {
   const E* x = static_cast<const E*>(a.x) + b * a.batch_stride;
   const int lc = (tid % LPR) * 8;
   const int64_t c = c0 + lc;
+  // all of the tile's loads are under way before the first value is used
+  Raw8<DT> raw8[TR / RPP];
+#pragma unroll
+  for (int i = 0; i < TR / RPP; ++i) {
+    const int64_t row = src[i * RPP + tid / LPR];
+    if (row >= 0 && c < a.cols)
+      raw8[i].load(x + row * a.row_stride + c, a.cols - c, a.vec);
+    else
+      raw8[i] = Raw8<DT>{};
+  }
 #pragma unroll
   for (int i = 0; i < TR / RPP; ++i) {
     const int r = i * RPP + tid / LPR;
-    const int64_t row = src[r];
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (row >= 0 && c < a.cols) load8<DT>(x + row * a.row_stride + c, a.cols - c, a.vec, v);
     if constexpr (WITH_ROWS) {
+      const int64_t row = src[r];
+      float v[8];
+      raw8[i].values(v);
       const uint32_t sb = scale_byte(max4(amax8(v)));
       if (row >= 0 && c < a.cb * 32) {
         const int64_t o = b * a.rows + row;
@@ -128,18 +138,7 @@ __global__ __launch_bounds__(2 * PACK_ROWS) void pack_cols_k(PackArgs a) {
     // LDS holds the input's own bits
     const int w0 = lc / PER;
 #pragma unroll
-    for (int w = 0; w < 8 / PER; ++w) {
-      uint32_t bits;
-      if constexpr (PER == 1) {
-        bits = __float_as_uint(v[w]);
-      } else if constexpr (DT == MOE_BF16) {
-        bits = (__float_as_uint(v[2 * w]) >> 16) | (__float_as_uint(v[2 * w + 1]) & 0xffff0000u);
-      } else {
-        const f16x2_t h = {static_cast<_Float16>(v[2 * w]), static_cast<_Float16>(v[2 * w + 1])};
-        __builtin_memcpy(&bits, &h, 4);
-      }
-      tile[r * 64 + ((w0 + w + 8 * (r >> 5)) & 63)] = bits;
-    }
+    for (int w = 0; w < 8 / PER; ++w) tile[r * 64 + ((w0 + w + 8 * (r >> 5)) & 63)] = raw8[i].w[w];
   }
   __syncthreads();
   const int rb = tid % (TR / 32), word = tid / (TR / 32);

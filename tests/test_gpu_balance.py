@@ -217,7 +217,8 @@ def router64(x, w, s, ds):
 
 
 @pytest.mark.parametrize("T,d,n", [(1, 64, 1), (5, 64, 7), (64, 128, 64), (200, 512, 40),
-                                   (333, 192, 129), (130, 1024, 896), (700, 64, 1024)])
+                                   (333, 192, 129), (130, 1024, 896), (700, 64, 1024), (200, 512, 80), (1, 64, 1024),
+                                   (1024, 64, 5)])
 def test_router_backward(T, d, n):
     import sparse_moe_ffn_sigmoid_amd as moe
     rng = np.random.default_rng(T + d + n)

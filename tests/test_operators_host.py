@@ -115,7 +115,9 @@ def test_product_refusals(moe):
         assert mm(**bad) == -1, bad
     for bad in (dict(dt=moe.MOE_MXFP4), dict(off=FAKE, G=1025), dict(N=(1 << 30) + 1, ldo=1 << 31)):
         assert mm(**bad) == -2, bad
-    assert mm(M=0, R=0) == 0
+    assert mm(M=0, R=0) == 0 and mm(M=0, R=0, rows=FAKE) == 0
+    assert mm(R=0, rows=FAKE) == -1                     # nothing to gather from
+    assert mm(M=(1 << 24) + 1, R=1, rows=FAKE, off=FAKE, G=8) == -2
 
     def kg(ac=FAKE, as_=FAKE, bc=FAKE, bs=FAKE, M=8, N=16, K=64, off=None, G=1, out=FAKE,
            dt=moe.MOE_F32):
@@ -136,7 +138,8 @@ def test_product_refusals(moe):
 
     for bad in (dict(x=None), dict(rs=63), dict(wc=None), dict(ws=None), dict(K=33), dict(M=9),
                 dict(out=None), dict(ldo=8), dict(wk=None), dict(wk=ODD), dict(wc=ODD),
-                dict(off=FAKE, G=0), dict(x=ctypes.c_void_p((1 << 20) + 1))):
+                dict(off=FAKE, G=0), dict(x=ctypes.c_void_p((1 << 20) + 1)),
+                dict(R=0, rows=FAKE)):
         assert lin(**bad) == -1, bad
     assert lin(xt=moe.MOE_MXFP4_A8) == -2 and lin(dt=4) == -2
     assert lin(nb=need - 1) == -3 and lin(M=0) == 0
