@@ -417,7 +417,8 @@ int moe_latent_backward_train(const moe_shape_t* shape, const moe_weights_t* wei
  *            same pass over the scores.  Rows of tokens that are not counted
  *            are zero.  May not overlap the inputs
  *   workspace: >= moe_balance_loss_workspace_bytes(T, n_seq) bytes, 256-byte
- *            aligned
+ *            aligned.  Small batches need none: NULL is taken, and
+ *            MOE_EWORKSPACE returned where the call needs one
  * Results do not depend on the order in which blocks run.
  */
 size_t moe_balance_loss_workspace_bytes(int32_t T, int32_t n_seq);
@@ -450,10 +451,11 @@ int moe_balance_loss_backward(const float* scores, int64_t ld_scores, int32_t T,
  *   dx [T][d] bf16, d_w_router [n][d] f32, d_router_logit_offset [n] f32;
  *            each may be NULL
  *   workspace: >= moe_router_backward_workspace_bytes(T, d, n) bytes, 256-byte
- *            aligned
- * The products run on the bf16 MFMA with fp32 accumulation: d_w_router from
- * the exact split of g into three bf16 parts, dx (a bf16 output) from two parts
- * of g and of W_r.  Deterministic.
+ *            aligned.  Small layers need none: NULL is taken, and
+ *            MOE_EWORKSPACE returned where the call needs one
+ * Large layers multiply on the bf16 MFMA with fp32 accumulation: d_w_router
+ * from the exact split of g into three bf16 parts, dx (a bf16 output) from two
+ * parts of g and of W_r.  Small ones run in fp32.  Deterministic.
  */
 size_t moe_router_backward_workspace_bytes(int32_t T, int32_t d, int32_t n);
 
@@ -549,7 +551,8 @@ int moe_mxfp4_matmul_kgroup(const uint8_t* a_codes, const uint8_t* a_scales,
  * moe_mxfp4_pack followed by moe_mxfp4_matmul, up to the order of the sums over
  * K.  A few rows (a token being decoded) are packed in registers, in one launch.
  *   workspace: >= moe_mxfp4_linear_workspace_bytes(x_rows, K) bytes, 256-byte
- *            aligned
+ *            aligned.  A few rows without groups need none: NULL is taken, and
+ *            MOE_EWORKSPACE returned where the call needs one
  */
 size_t moe_mxfp4_linear_workspace_bytes(int64_t x_rows, int64_t K);
 

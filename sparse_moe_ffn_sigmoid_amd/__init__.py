@@ -285,23 +285,37 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _call(fn, dev, *args):
-    """fn(*args, stream) on the device's current stream; raises MoeError."""
+def _status(fn, dev, *args):
+    """fn(*args, stream) on the device's current stream."""
     stream = torch._C._cuda_getCurrentRawStream(dev.index)
     if dev.index == torch.cuda.current_device():
-        st = fn(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, stream)
+        return fn(*args, stream)
+    with torch.cuda.device(dev):
+        return fn(*args, stream)
+
+
+def _call(fn, dev, *args):
+    """As _status; raises MoeError."""
+    st = _status(fn, dev, *args)
     if st != 0:
         raise MoeError(st, fn.__name__)
 
 
-def _workspace(workspace, need, dev):
+def _call_scratch(fn, dev, few, need, workspace, *args):
+    """fn(*args, workspace, its bytes, stream).  Calls with few tokens may need
+    no workspace: they are made without one first, and the library asks for it
+    with MOE_EWORKSPACE before it launches anything.  need: (query, arguments)."""
+    if workspace is None and few:
+        st = _status(fn, dev, *args, None, 0)
+        if st == 0:
+            return
+        if st != -3:
+            raise MoeError(st, fn.__name__)
     if workspace is None:
-        return torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    _check(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
-    return workspace
+        workspace = torch.empty(max(need[0](*need[1:]), 256), dtype=torch.uint8, device=dev)
+    else:
+        _check(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    _call(fn, dev, *args, _addr(workspace), workspace.numel())
 
 
 def _score_rows(scores, name="scores"):
@@ -355,10 +369,11 @@ def balance_loss(scores: torch.Tensor, idx: torch.Tensor, seq_offsets=None, toke
                tokens=torch.empty(S, dtype=torch.int32, device=dev))
     if want_grad:
         out["dscores"] = torch.empty((T, n), dtype=torch.float32, device=dev)
-    ws = _workspace(workspace, _lib.moe_balance_loss_workspace_bytes(T, S), dev)
-    _call(_lib.moe_balance_loss, dev, _addr(scores), ld, T, n, k, _addr(idx), _addr(seq_offsets), S,
-          _addr(mask), _addr(dloss), _addr(out["loss"]), _addr(out["counts"]), _addr(out["tokens"]),
-          _addr(out.get("dscores")), _addr(ws), ws.numel())
+    _call_scratch(_lib.moe_balance_loss, dev, T <= 256,
+                  (_lib.moe_balance_loss_workspace_bytes, T, S), workspace, _addr(scores), ld, T,
+                  n, k, _addr(idx), _addr(seq_offsets), S, _addr(mask), _addr(dloss),
+                  _addr(out["loss"]), _addr(out["counts"]), _addr(out["tokens"]),
+                  _addr(out.get("dscores")))
     return out
 
 
@@ -403,11 +418,10 @@ def router_backward(x: torch.Tensor, w_router: torch.Tensor, scores: torch.Tenso
         for f, (dt, shape) in names.items():
             if into.get(f) is not None:
                 _check(into[f], f, dt, shape, dev)
-    need = _lib.moe_router_backward_workspace_bytes(T, d, n)
-    ws = _workspace(workspace, need, dev)
-    _call(_lib.moe_router_backward, dev, _addr(x), _addr(w_router), _addr(scores), _addr(dscores), T,
-          d, n, 0 if into is None else 1, *[_addr(out.get(f)) for f in names], _addr(ws),
-          ws.numel())
+    _call_scratch(_lib.moe_router_backward, dev, T <= 1024,
+                  (_lib.moe_router_backward_workspace_bytes, T, d, n), workspace, _addr(x),
+                  _addr(w_router), _addr(scores), _addr(dscores), T, d, n,
+                  0 if into is None else 1, *[_addr(out.get(f)) for f in names])
     return out
 
 
@@ -594,9 +608,10 @@ def mxfp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
     out_dtype = x.dtype if out_dtype is None else out_dtype
     dt = _mx_type(out_dtype, "out_dtype")
     out, ldo = _mx_out(out, M, N, out_dtype, dev)
-    ws = _workspace(workspace, _lib.moe_mxfp4_linear_workspace_bytes(R, K), dev)
-    _call(_lib.moe_mxfp4_linear, dev, _addr(x), xt, R, rs, _addr(w_codes), _addr(w_scales), M, N, K,
-          _addr(offsets), G, _addr(rows), _addr(out), dt, ldo, _addr(ws), ws.numel())
+    _call_scratch(_lib.moe_mxfp4_linear, dev, M <= 16,
+                  (_lib.moe_mxfp4_linear_workspace_bytes, R, K), workspace, _addr(x), xt, R, rs,
+                  _addr(w_codes), _addr(w_scales), M, N, K, _addr(offsets), G, _addr(rows),
+                  _addr(out), dt, ldo)
     return out
 
 

@@ -415,15 +415,17 @@ extern "C" int moe_balance_loss(const float* scores, int64_t ld_scores, int32_t 
   using namespace moe::balance;
   const int st = check(T, n, k, n_seq, seq_offsets, ld_scores);
   if (st != MOE_OK) return st;
-  if (!loss || !counts || !tokens || !workspace) return MOE_EINVAL;
+  if (!loss || !counts || !tokens) return MOE_EINVAL;
   if (T > 0 && (!scores || !topk_idx)) return MOE_EINVAL;
   if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MOE_EINVAL;
-  if (workspace_bytes < moe_balance_loss_workspace_bytes(T, n_seq)) return MOE_EWORKSPACE;
+  const bool small = is_small(T, n, n_seq);
+  if (!small && (!workspace || workspace_bytes < moe_balance_loss_workspace_bytes(T, n_seq)))
+    return MOE_EWORKSPACE;
   Args a{scores, ld_scores, T,      n,    k,       topk_idx, seq_offsets, n_seq, token_mask,
          dloss,  counts,    tokens, loss, dscores, static_cast<float*>(workspace),
          rows_per_wave(T)};
   hipStream_t hs = static_cast<hipStream_t>(stream);
-  if (is_small(T, n, n_seq)) return pass(a, true, hs);
+  if (small) return pass(a, true, hs);
   const int64_t cells = static_cast<int64_t>(n_seq) * n;
   hipLaunchKernelGGL(clear_k, dim3(static_cast<unsigned>(std::min<int64_t>((cells + 255) / 256, 4096))),
                      dim3(256), 0, hs, a);

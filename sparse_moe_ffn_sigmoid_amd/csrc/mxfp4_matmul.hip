@@ -978,8 +978,7 @@ extern "C" int moe_mxfp4_linear(const void* x, int32_t x_dtype, int64_t x_rows,
   if ((!x && x_rows > 0) || reinterpret_cast<uintptr_t>(x) % size != 0 || !w_codes || !w_scales ||
       !aligned16(w_codes))
     return MOE_EINVAL;
-  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MOE_EINVAL;
-  if (workspace_bytes < moe_mxfp4_linear_workspace_bytes(x_rows, K)) return MOE_EWORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MOE_EINVAL;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (!row_offsets && M <= 16 && fused_bytes(M, K) <= FUSED_BYTES && aligned16(x) &&
       row_stride * size % 16 == 0) {
@@ -1000,6 +999,8 @@ extern "C" int moe_mxfp4_linear(const void* x, int32_t x_dtype, int64_t x_rows,
     if (x_dtype == MOE_BF16) return launch_fused<MOE_BF16>(a, x, row_stride, st);
     return launch_fused<MOE_F16>(a, x, row_stride, st);
   }
+  if (!workspace || workspace_bytes < moe_mxfp4_linear_workspace_bytes(x_rows, K))
+    return MOE_EWORKSPACE;
   moe::Carver cv(workspace);
   uint8_t* codes = cv.take<uint8_t>(x_rows * (K / 2));
   uint8_t* scales = cv.take<uint8_t>(x_rows * (K / 32));

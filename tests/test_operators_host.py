@@ -20,25 +20,25 @@ def moe():
 
 def test_balance_loss_refusals(moe):
     lib = moe.lib()
-    need = lib.moe_balance_loss_workspace_bytes(100, 3)
-    assert need >= 4 * 103 and need % 256 == 0
+    need = lib.moe_balance_loss_workspace_bytes(2000, 3)
+    assert need >= 4 * 2003 and need % 256 == 0
     assert lib.moe_balance_loss_workspace_bytes(0, 1) > 0
     assert lib.moe_balance_loss_workspace_bytes(-1, 1) == 0
     assert lib.moe_balance_loss_workspace_bytes(10, 0) == 0
     assert lib.moe_balance_loss_workspace_bytes((1 << 20) + 1, 1) == 0
 
-    def call(T=100, n=64, k=4, ld=64, S=3, scores=FAKE, idx=FAKE, off=FAKE, loss=FAKE, counts=FAKE,
+    def call(T=2000, n=64, k=4, ld=64, S=3, scores=FAKE, idx=FAKE, off=FAKE, loss=FAKE, counts=FAKE,
              tokens=FAKE, ws=FAKE, nb=need):
         return lib.moe_balance_loss(scores, ld, T, n, k, idx, off, S, None, None, loss, counts,
                                     tokens, None, ws, nb, None)
 
     for bad in (dict(T=-1), dict(n=0), dict(k=0), dict(k=65), dict(ld=63), dict(S=0),
                 dict(off=None), dict(scores=None), dict(idx=None), dict(loss=None),
-                dict(counts=None), dict(tokens=None), dict(ws=None), dict(ws=ODD)):
+                dict(counts=None), dict(tokens=None), dict(ws=ODD)):
         assert call(**bad) == -1, bad
     assert call(n=1025, ld=1025) == -2
     assert call(T=(1 << 20) + 1) == -2
-    assert call(nb=need - 256) == -3
+    assert call(nb=need - 256) == -3 and call(ws=None, nb=0) == -3
 
     def back(T=100, n=64, k=4, ld=64, S=3, scores=FAKE, counts=FAKE, tokens=FAKE, off=FAKE,
              d=FAKE):
@@ -53,21 +53,21 @@ def test_balance_loss_refusals(moe):
 
 def test_router_backward_refusals(moe):
     lib = moe.lib()
-    need = lib.moe_router_backward_workspace_bytes(100, 128, 40)
+    need = lib.moe_router_backward_workspace_bytes(3000, 128, 40)
     assert need > 0 and lib.moe_router_backward_workspace_bytes(0, 128, 40) > 0
     for bad in ((-1, 128, 40), (100, 96, 40), (100, 0, 40), (100, 128, 0), (100, 128, 1025),
                 ((1 << 20) + 1, 128, 40)):
         assert lib.moe_router_backward_workspace_bytes(*bad) == 0, bad
 
-    def call(T=100, d=128, n=40, x=FAKE, w=FAKE, s=FAKE, ds=FAKE, dx=FAKE, dw=FAKE, ws=FAKE,
+    def call(T=3000, d=128, n=40, x=FAKE, w=FAKE, s=FAKE, ds=FAKE, dx=FAKE, dw=FAKE, ws=FAKE,
              nb=need):
         return lib.moe_router_backward(x, w, s, ds, T, d, n, 0, dx, dw, FAKE, ws, nb, None)
 
     for bad in (dict(T=-1), dict(d=100), dict(n=0), dict(x=None), dict(w=None), dict(s=None),
-                dict(ds=None), dict(ws=None), dict(ws=ODD), dict(dx=ODD), dict(dw=ODD)):
+                dict(ds=None), dict(ws=ODD), dict(dx=ODD), dict(dw=ODD)):
         assert call(**bad) == -1, bad
     assert call(n=2000) == -2
-    assert call(nb=need - 1) == -3
+    assert call(nb=need - 1) == -3 and call(ws=None, nb=0) == -3
 
 
 def test_pack_refusals(moe):
@@ -128,21 +128,21 @@ def test_product_refusals(moe):
         assert kg(**bad) == -1, bad
     assert kg(dt=9) == -2 and kg(off=FAKE, G=1025) == -2
 
-    need = lib.moe_mxfp4_linear_workspace_bytes(8, 64)
-    assert need >= 8 * 34 and lib.moe_mxfp4_linear_workspace_bytes(8, 40) == 0
+    need = lib.moe_mxfp4_linear_workspace_bytes(80, 64)
+    assert need >= 80 * 34 and lib.moe_mxfp4_linear_workspace_bytes(8, 40) == 0
 
-    def lin(x=FAKE, xt=moe.MOE_BF16, R=8, rs=64, wc=FAKE, ws=FAKE, M=8, N=16, K=64, off=None, G=1,
+    def lin(x=FAKE, xt=moe.MOE_BF16, R=80, rs=64, wc=FAKE, ws=FAKE, M=80, N=16, K=64, off=None, G=1,
             rows=None, out=FAKE, dt=moe.MOE_BF16, ldo=16, wk=FAKE, nb=need):
         return lib.moe_mxfp4_linear(x, xt, R, rs, wc, ws, M, N, K, off, G, rows, out, dt, ldo, wk,
                                     nb, None)
 
-    for bad in (dict(x=None), dict(rs=63), dict(wc=None), dict(ws=None), dict(K=33), dict(M=9),
-                dict(out=None), dict(ldo=8), dict(wk=None), dict(wk=ODD), dict(wc=ODD),
+    for bad in (dict(x=None), dict(rs=63), dict(wc=None), dict(ws=None), dict(K=33), dict(M=81),
+                dict(out=None), dict(ldo=8), dict(wk=ODD), dict(wc=ODD),
                 dict(off=FAKE, G=0), dict(x=ctypes.c_void_p((1 << 20) + 1)),
                 dict(R=0, rows=FAKE)):
         assert lin(**bad) == -1, bad
     assert lin(xt=moe.MOE_MXFP4_A8) == -2 and lin(dt=4) == -2
-    assert lin(nb=need - 1) == -3 and lin(M=0) == 0
+    assert lin(nb=need - 1) == -3 and lin(wk=None, nb=0) == -3 and lin(M=0) == 0
 
 
 def test_python_refusals(moe):
