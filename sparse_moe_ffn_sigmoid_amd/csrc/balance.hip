@@ -381,11 +381,11 @@ static int pass(const Args& a, bool small, hipStream_t st) {
   return MOE_OK;
 }
 
-// One block's work against three more launches: 64 x 896 takes 17 us a call here
-// and 25 in four launches, 256 x 256 in 4 sequences 21 against 25; with 1024
-// tokens (33) or 8 sequences (40 to 53) the one block is the slower.
+// One block's work against three more launches, us a call: 128 x 896 14.3 against
+// 26.4, 256 x 512 14.4 against 24.5, in four sequences 25.3 against 24.6; with
+// 1024 tokens (33) or 8 sequences (40 to 53) the one block is the slower.
 static bool is_small(int T, int n, int S) {
-  return T <= 256 && static_cast<int64_t>(T) * n <= 65536 && S <= 4;
+  return T <= 256 && static_cast<int64_t>(T) * n <= 131072 && S <= 4;
 }
 
 // Tokens per wave: 16 waves on each of 256 compute units.
