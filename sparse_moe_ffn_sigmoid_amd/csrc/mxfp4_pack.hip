@@ -13,7 +13,9 @@
 // ([columns][rows/2]), K-contiguous again: the operands of a product that
 // contracts over the rows (dx and dW of a linear layer).  One read of the
 // input serves both.  Everything here is bound by memory: 2 or 4 bytes per
-// element in and 17/32 of a byte out per direction.
+// element in and 17/32 of a byte out per direction.  bf16 16,384 x 7168 both ways:
+// 105 us for 360 MB (3.4 TB/s); 24 x 2048 x 3584 both ways: 118 us for 539 MB (4.6
+// TB/s, a large copy's rate); unpacking 16,384 x 7168: 50 us for 297 MB (5.9 TB/s).
 #include <algorithm>
 
 #include "common.hpp"

@@ -4,11 +4,14 @@
 //   dx = g W_r  [T][d],   dW_r = g^T x  [n][d],   d_offset = sum_t g  [n]
 //
 // Two products of 2 T n d operations each on the bf16 MFMA.  Their operands
-// are written K-contiguous once by the kernels here (g both ways, W_r and x
-// transposed), a few per cent of the products' time.  dW_r is an fp32 output:
+// are written K-contiguous first, in one launch (g both ways, W_r and x
+// transposed).  dW_r is an fp32 output:
 // g enters it as the exact sum of three bf16 parts (24 bits), three segments of
 // one contraction against the same bf16 x.  dx is rounded to bf16: two parts of
 // g and of W_r (16 bits each) are kept, without the product of the low parts.
+//
+// T = 4096, d = 7168, n = 896: 428 us; the products take 236 us (dW_r) and 203 us
+// (dx) on their own, 158 GFLOP of bf16 each, 0.67 and 0.78 PFLOP/s, and bound it.
 #include <algorithm>
 
 #include "common.hpp"
@@ -36,26 +39,29 @@ __device__ __forceinline__ void store8(bf16_t* p, const bf16_t (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = q;
 }
 
+struct Prep {
+  const float *scores, *dscores, *w;
+  const bf16_t* x;
+  int T, n, d;
+  int64_t np, Tp;
+  bf16_t *g_hi, *g_lo, *gt_hi, *gt_mid, *gt_lo, *wt_hi, *wt_lo, *xt;
+  float* part;
+  // blocks of each kind, in this order: scores, x, W_r
+  int score_blocks, x_blocks;
+};
+
 // g of 64 tokens x 64 experts: by token [T][np] in two parts, by expert [n][Tp]
 // in three, zeros behind the ends, and the tile's sum per expert.
-__global__ __launch_bounds__(256) void score_grad_k(const float* __restrict__ scores,
-                                                    const float* __restrict__ dscores, int T,
-                                                    int n, int64_t np, int64_t Tp,
-                                                    bf16_t* __restrict__ g_hi,
-                                                    bf16_t* __restrict__ g_lo,
-                                                    bf16_t* __restrict__ gt_hi,
-                                                    bf16_t* __restrict__ gt_mid,
-                                                    bf16_t* __restrict__ gt_lo,
-                                                    float* __restrict__ part) {
-  __shared__ float tile[TILE][TILE + 1];
-  const int e0 = blockIdx.x * TILE, t0 = blockIdx.y * TILE;
+__device__ __forceinline__ void score_tile(const Prep& p, int e0, int tt, float* lds) {
+  auto tile = reinterpret_cast<float(*)[TILE + 1]>(lds);
+  const int t0 = tt * TILE;
   for (int i = threadIdx.x; i < TILE * TILE; i += 256) {
     const int t = i / TILE, e = i % TILE;
     float g = 0.f;
-    if (t0 + t < T && e0 + e < n) {
-      const int64_t at = static_cast<int64_t>(t0 + t) * n + e0 + e;
-      const float s = scores[at];
-      g = dscores[at] * (s * (1.f - s));
+    if (t0 + t < p.T && e0 + e < p.n) {
+      const int64_t at = static_cast<int64_t>(t0 + t) * p.n + e0 + e;
+      const float s = p.scores[at];
+      g = p.dscores[at] * (s * (1.f - s));
     }
     tile[t][e] = g;
   }
@@ -63,31 +69,31 @@ __global__ __launch_bounds__(256) void score_grad_k(const float* __restrict__ sc
   for (int i = threadIdx.x; i < TILE * TILE / 8; i += 256) {
     const int r = i / 8, c = i % 8 * 8;
     bf16_t hi[8], mid[8], lo[8];
-    if (t0 + r < T) {
+    if (t0 + r < p.T) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) split2(tile[r][c + j], hi[j], lo[j]);
-      const int64_t at = static_cast<int64_t>(t0 + r) * np + e0 + c;
-      store8(g_hi + at, hi);
-      store8(g_lo + at, lo);
+      const int64_t at = static_cast<int64_t>(t0 + r) * p.np + e0 + c;
+      store8(p.g_hi + at, hi);
+      store8(p.g_lo + at, lo);
     }
-    if (e0 + r < n) {
+    if (e0 + r < p.n) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float v = tile[c + j][r];
         split2(v, hi[j], mid[j]);
         lo[j] = f32_to_bf16((v - bf16_to_f32(hi[j])) - bf16_to_f32(mid[j]));
       }
-      const int64_t at = (e0 + r) * Tp + t0 + c;
-      store8(gt_hi + at, hi);
-      store8(gt_mid + at, mid);
-      store8(gt_lo + at, lo);
+      const int64_t at = (e0 + r) * p.Tp + t0 + c;
+      store8(p.gt_hi + at, hi);
+      store8(p.gt_mid + at, mid);
+      store8(p.gt_lo + at, lo);
     }
   }
   if (threadIdx.x < TILE) {
     float sum = 0.f;
 #pragma unroll 8
     for (int t = 0; t < TILE; ++t) sum += tile[t][threadIdx.x];
-    part[blockIdx.y * np + e0 + threadIdx.x] = sum;
+    p.part[tt * p.np + e0 + threadIdx.x] = sum;
   }
 }
 
@@ -97,12 +103,10 @@ __global__ __launch_bounds__(256) void score_grad_k(const float* __restrict__ sc
 constexpr int TROWS = 128;
 
 template <typename IN>
-__global__ __launch_bounds__(256) void transpose_k(const IN* __restrict__ in, int R, int C,
-                                                   int64_t ld_out, bf16_t* __restrict__ hi,
-                                                   bf16_t* __restrict__ lo) {
+__device__ __forceinline__ void transpose_tile(const IN* in, int R, int C, int64_t ld_out,
+                                               bf16_t* hi, bf16_t* lo, int c0, int r0, void* lds) {
   constexpr int PER = 16 / sizeof(IN), LPR = TILE / PER;  // elements per load, lanes per row
-  __shared__ IN tile[TROWS][TILE + 1];
-  const int c0 = blockIdx.x * TILE, r0 = blockIdx.y * TROWS;
+  auto tile = reinterpret_cast<IN(*)[TILE + 1]>(lds);
 #pragma unroll
   for (int i = threadIdx.x; i < TROWS * LPR; i += 256) {
     const int r = i / LPR, c = i % LPR * PER;
@@ -129,6 +133,25 @@ __global__ __launch_bounds__(256) void transpose_k(const IN* __restrict__ in, in
     }
     store8(hi + at, h);
   }
+}
+
+// All operands of the products in one launch: g both ways, x and W_r transposed.
+__global__ __launch_bounds__(256) void prepare_k(Prep p) {
+  __shared__ __attribute__((aligned(16))) float lds[TROWS * (TILE + 1)];
+  int b = blockIdx.x;
+  if (b < p.score_blocks) {
+    const int tn = static_cast<int>(p.np / TILE);
+    score_tile(p, b % tn * TILE, b / tn, lds);
+    return;
+  }
+  b -= p.score_blocks;
+  const int td = p.d / TILE;
+  if (b < p.x_blocks) {
+    transpose_tile<bf16_t>(p.x, p.T, p.d, p.Tp, p.xt, nullptr, b % td * TILE, b / td * TROWS, lds);
+    return;
+  }
+  b -= p.x_blocks;
+  transpose_tile<float>(p.w, p.n, p.d, p.np, p.wt_hi, p.wt_lo, b % td * TILE, b / td * TROWS, lds);
 }
 
 // A small layer in one launch, in fp32: a block takes CW columns of x, dx, W_r
@@ -248,9 +271,9 @@ static size_t layout(int T, int d, int n, Workspace* out, void* base) {
   return cv.bytes();
 }
 
-// What one launch of fp32 multiply-adds does sooner than seven: 200 tokens x 512 x
-// 40 experts take 11.6 us against 40.0, 64 x 512 x 256 23.7 against 38.3, 1024 x
-// 256 x 20 41.1 against 41.4.
+// What one launch of fp32 multiply-adds does sooner than four: 200 tokens x 512 x
+// 40 experts take 11.5 us against 32.2, 64 x 512 x 256 23.6 against 29.5, 1024 x
+// 256 x 20 33.1 against 33.1.
 static bool is_small(int T, int d, int n) {
   return small_bytes(T, n) <= 96 * 1024 && static_cast<int64_t>(T) * n * d <= (8 << 20);
 }
@@ -329,20 +352,20 @@ extern "C" int moe_router_backward(const void* x, const float* w_router, const f
     MOE_LAUNCH_CHECK();
     return MOE_OK;
   }
-  const unsigned tn = static_cast<unsigned>(np / 64), tt = static_cast<unsigned>(Tp / 64),
-                 td = static_cast<unsigned>(d / 64);
-  hipLaunchKernelGGL(score_grad_k, dim3(tn, tt), dim3(256), 0, st, scores, dscores, T, n, np, Tp,
-                     w.g_hi, w.g_lo, w.gt_hi, w.gt_mid, w.gt_lo, w.part);
+  const int64_t tn = np / TILE, tt = Tp / TILE, td = d / TILE;
+  Prep p{scores, dscores, w_router, static_cast<const bf16_t*>(x), T, n, d, np, Tp, w.g_hi, w.g_lo,
+         w.gt_hi, w.gt_mid, w.gt_lo, w.wt_hi, w.wt_lo, w.xt, w.part, 0, 0};
+  p.score_blocks = static_cast<int>(tn * tt);
+  p.x_blocks = d_w_router ? static_cast<int>(td * ((tt + 1) / 2)) : 0;
+  const int w_blocks = dx ? static_cast<int>(td * ((tn + 1) / 2)) : 0;
+  hipLaunchKernelGGL(prepare_k, dim3(p.score_blocks + p.x_blocks + w_blocks), dim3(256), 0, st, p);
   MOE_LAUNCH_CHECK();
   if (d_router_logit_offset) {
-    hipLaunchKernelGGL(offset_k, dim3(tn), dim3(256), 0, st, w.part, static_cast<int>(tt), n, np,
-                       accumulate, d_router_logit_offset);
+    hipLaunchKernelGGL(offset_k, dim3(static_cast<unsigned>(tn)), dim3(256), 0, st, w.part,
+                       static_cast<int>(tt), n, np, accumulate, d_router_logit_offset);
     MOE_LAUNCH_CHECK();
   }
   if (d_w_router) {
-    hipLaunchKernelGGL(transpose_k<bf16_t>, dim3(td, (tt + 1) / 2), dim3(256), 0, st,
-                       static_cast<const bf16_t*>(x), T, d, Tp, w.xt, nullptr);
-    MOE_LAUNCH_CHECK();
     rc = product3(w, {w.gt_hi, w.gt_mid, w.gt_lo}, {w.xt, w.xt, w.xt}, Tp, n, d,
                   accumulate ? w.sum : d_w_router, gemm::EPI_F32, st);
     if (rc != MOE_OK) return rc;
@@ -352,9 +375,6 @@ extern "C" int moe_router_backward(const void* x, const float* w_router, const f
     }
   }
   if (dx) {
-    hipLaunchKernelGGL(transpose_k<float>, dim3(td, (tn + 1) / 2), dim3(256), 0, st, w_router, n, d, np,
-                       w.wt_hi, w.wt_lo);
-    MOE_LAUNCH_CHECK();
     rc = product3(w, {w.g_hi, w.g_hi, w.g_lo}, {w.wt_hi, w.wt_lo, w.wt_hi}, np, T, d,
                   accumulate ? static_cast<void*>(w.sum) : dx,
                   accumulate ? gemm::EPI_F32 : gemm::EPI_BF16, st);
