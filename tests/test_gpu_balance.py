@@ -307,3 +307,49 @@ def test_balance_loss_in_a_training_step():
     with pytest.raises(ValueError):
         moe.latent_backward_train(sh, w, x, f2["scores"], f2["idx"], f2["w"], dout, saved, lr=0.1,
                                   dscores=b["dscores"])
+
+
+def test_balance_rows_beyond_4_gib():
+    import sparse_moe_ffn_sigmoid_amd as moe
+    T, n, k = 1 << 20, 1024, 2                              # 4.3 GB of scores
+    announce("balance 2^20 x 1024")
+    s = torch.zeros((T, n), device="cuda")
+    s[:, :7] = 0.25
+    s[-3:] = torch.rand((3, n), generator=torch.Generator("cuda").manual_seed(1), device="cuda")
+    idx = torch.zeros((T, k), dtype=torch.int32, device="cuda")
+    idx[:, 1] = torch.arange(T, device="cuda") % n
+    off = torch.tensor([0, T - 3, T], dtype=torch.int32, device="cuda")
+    r = moe.balance_loss(s, idx, seq_offsets=off, want_grad=True)
+    loss, counts, tokens, grad, size = balance64(s[-3:].cpu().numpy(), idx[-3:].cpu().numpy())
+    assert np.array_equal(r["counts"][1].cpu().numpy(), counts[0]) and r["tokens"].tolist() == [T - 3, 3]
+    assert r["counts"][0].sum().item() == (T - 3) * k
+    row, chain = rounds(T, n)
+    assert abs(r["loss"][1].item() - loss[0]) <= (row + chain) * U32 * loss[0]
+    assert (np.abs(as64(r["dscores"][-3:]) - grad) <= (row + 8) * U32 * size + 1e-44).all()
+    with pytest.raises(moe.MoeError):
+        moe.balance_loss(s, idx, seq_offsets=off, workspace=torch.empty(256, dtype=torch.uint8,
+                                                                        device="cuda"))
+
+
+def test_balance_refusals_on_the_device():
+    import sparse_moe_ffn_sigmoid_amd as moe
+    announce("balance refusals")
+    s = torch.rand((8, 16), device="cuda")
+    i = torch.zeros((8, 2), dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    for bad in (lambda: moe.balance_loss(s.double(), i), lambda: moe.balance_loss(s[0], i),
+                lambda: moe.balance_loss(s[:, ::2], i), lambda: moe.balance_loss(s, i.long()),
+                lambda: moe.balance_loss(s, i[:4]), lambda: moe.balance_loss(s, i.cpu()),
+                lambda: moe.balance_loss(s, i, seq_offsets=off.long()),
+                lambda: moe.balance_loss(s, i, token_mask=torch.ones(7, dtype=torch.bool,
+                                                                     device="cuda")),
+                lambda: moe.balance_loss(s, i, seq_offsets=off, dloss=torch.ones(2, device="cuda")),
+                lambda: moe.balance_loss_backward(s, i, off, 2),
+                lambda: moe.router_backward(s, s, s, s),
+                lambda: moe.router_backward(s.bfloat16(), s, s, s)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: moe.balance_loss(torch.rand((4, 1025), device="cuda"), i[:4]),
+                lambda: moe.balance_loss(s[:, :1], i)):       # more choices than experts
+        with pytest.raises(moe.MoeError):
+            bad()

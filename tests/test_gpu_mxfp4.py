@@ -427,3 +427,115 @@ def test_experts_run_of_the_operators():
     o, at = off.tolist(), rows.cpu().numpy()
     for e in range(n):
         check_product(y[o[e]:o[e + 1]], a[at[o[e]:o[e + 1]]], wv[e], F32)
+
+
+def random_codes(*shape):
+    g = torch.Generator("cuda").manual_seed(sum(shape))
+    return torch.randint(0, 256, shape, dtype=torch.uint8, device="cuda", generator=g)
+
+
+def test_weights_beyond_4_gib():
+    import sparse_moe_ffn_sigmoid_amd as moe
+    G, N, K = 1024, 2080, 4096                     # 4.4 GB of codes
+    announce("weights beyond 4 GiB")
+    codes = torch.zeros((G, N, K // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.full((G, N, K // 32), 120, dtype=torch.uint8, device="cuda")
+    for g in (5, G - 1):
+        codes[g] = random_codes(N, K // 2)
+    for few, many in ((3, 40), (300, 20000)):      # a few rows per group, and many
+        off = torch.zeros(G + 1, dtype=torch.int32, device="cuda")
+        off[6:] = few
+        off[G] = few + many
+        x = operand(few + many, K, few)
+        y = moe.mxfp4_linear(x.cuda(), codes, scales, offsets=off, out_dtype=F32)
+        for g, rows in ((5, slice(0, few)), (G - 1, slice(few + many - 33, few + many))):
+            b = mx_decode64(nibbles(codes[g]), scales[g].cpu().numpy())
+            check_product(y[rows], mx_round64(as64(x[rows])), b, F32)
+
+
+def test_gathered_rows_beyond_4_gib():
+    import sparse_moe_ffn_sigmoid_amd as moe
+    R, K, N, M = 2_200_000, 4096, 70, 200          # 4.5 GB of codes
+    announce("gathered rows beyond 4 GiB")
+    codes = torch.zeros((R, K // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.full((R, K // 32), 125, dtype=torch.uint8, device="cuda")
+    codes[R - 50:] = random_codes(50, K // 2)
+    rows = torch.from_numpy(np.random.default_rng(0).integers(R - 50, R, M).astype(np.int32))
+    rows[7], rows[150] = R, -5
+    w = operand(N, K, 2)
+    p = moe.mxfp4_pack(w.cuda())
+    y = moe.mxfp4_matmul(codes, scales, p["codes"], p["scales"], rows=rows.cuda(), out_dtype=F32)
+    last = mx_decode64(nibbles(codes[R - 50:]), scales[R - 50:].cpu().numpy())
+    a = np.concatenate([last, np.zeros((1, K))])
+    at = rows.numpy() - (R - 50)
+    at[[7, 150]] = 50
+    check_product(y, a[at], mx_round64(as64(w)), F32)
+
+
+def test_output_beyond_32_bits():
+    import sparse_moe_ffn_sigmoid_amd as moe
+    M, N, K = 70001, 32768, 64                     # 2.3e9 outputs
+    announce("outputs beyond 2^31")
+    x, w = operand(M, K, 1), operand(N, K, 2)
+    p = moe.mxfp4_pack(w.cuda())
+    y = moe.mxfp4_linear(x.cuda(), p["codes"], p["scales"])
+    rows = [0, 65535, 65536, 69999, 70000]
+    check_product(y[rows][:, -300:], mx_round64(as64(x[rows])), mx_round64(as64(w[-300:])), BF16)
+
+
+def test_products_on_two_streams_and_given_buffers():
+    import sparse_moe_ffn_sigmoid_amd as moe
+    N, K = 300, 512
+    announce("two streams")
+    w = operand(N, K, 1)
+    p = moe.mxfp4_pack(w.cuda())
+    b = mx_round64(as64(w))
+    xs = [operand(M, K, M).cuda() for M in (1, 100, 400, 9)]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    ys = []
+    for x, s in zip(xs, streams):
+        with torch.cuda.stream(s):
+            ys.append([moe.mxfp4_linear(x, p["codes"], p["scales"], out_dtype=F32)
+                       for _ in range(5)])
+    torch.cuda.synchronize()
+    for x, many in zip(xs, ys):
+        for y in many:
+            check_product(y, mx_round64(as64(x)), b, F32)
+    ws = torch.empty(moe.lib().moe_mxfp4_linear_workspace_bytes(400, K), dtype=torch.uint8,
+                     device="cuda")
+    y = moe.mxfp4_linear(xs[2], p["codes"], p["scales"], out_dtype=F32, workspace=ws)
+    assert torch.equal(y, ys[2][0])
+    with pytest.raises(moe.MoeError, match="workspace"):
+        moe.mxfp4_linear(xs[2], p["codes"], p["scales"], workspace=ws[:1024])
+
+
+def test_python_refusals_on_the_device():
+    import sparse_moe_ffn_sigmoid_amd as moe
+    announce("refusals")
+    x = operand(8, 64, 1).cuda()
+    p = moe.mxfp4_pack(x)
+    c, s = p["codes"], p["scales"]
+    off = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    for bad in (lambda: moe.mxfp4_pack(x.double()), lambda: moe.mxfp4_pack(x[:, ::2]),
+                lambda: moe.mxfp4_pack(x[0]), lambda: moe.mxfp4_pack(x, rows=False),
+                lambda: moe.mxfp4_pack(x, offsets=off),
+                lambda: moe.mxfp4_pack(x, cols=True, offsets=off.long()),
+                lambda: moe.mxfp4_pack(x.expand(2, 8, 64), cols=True, offsets=off),
+                lambda: moe.mxfp4_unpack(c, s, 32), lambda: moe.mxfp4_unpack(c, s, 65),
+                lambda: moe.mxfp4_unpack(c, s[:4], 64),
+                lambda: moe.mxfp4_unpack(c, s, 64, torch.float64),
+                lambda: moe.mxfp4_matmul(c, s, c[:, :16].contiguous(), s[:, :1].contiguous()),
+                lambda: moe.mxfp4_matmul(c, s, c, s, offsets=off),
+                lambda: moe.mxfp4_matmul(c, s, c[None], s[None]),
+                lambda: moe.mxfp4_matmul(c, s, c, s, out_dtype=torch.int32),
+                lambda: moe.mxfp4_matmul(c, s, c, s, out=torch.empty((8, 7), device="cuda")),
+                lambda: moe.mxfp4_matmul(c, s, c, s, rows=off.long()),
+                lambda: moe.mxfp4_matmul_kgroup(c, s, c[:, :16].contiguous(), s[:, :1].contiguous()),
+                lambda: moe.mxfp4_linear(x[:, :48], c, s), lambda: moe.mxfp4_linear(x[0], c, s)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(moe.MoeError):                       # nothing to gather from
+        moe.mxfp4_linear(x[:0], c, s, rows=off)
+    with pytest.raises(moe.MoeError):
+        moe.mxfp4_pack(x, cols=True, offsets=torch.zeros(1026, dtype=torch.int32, device="cuda"))
