@@ -539,3 +539,79 @@ def test_python_refusals_on_the_device():
         moe.mxfp4_linear(x[:0], c, s, rows=off)
     with pytest.raises(moe.MoeError):
         moe.mxfp4_pack(x, cols=True, offsets=torch.zeros(1026, dtype=torch.int32, device="cuda"))
+
+
+def sampled_rows(M, edges, seed):
+    """Row numbers at and around multiples of the tile heights, and others."""
+    near = {r + d for e in edges for r in range(0, M + 1, e) for d in (-1, 0, 1, 31, 32)}
+    other = np.random.default_rng(seed).integers(0, M, 40).tolist()
+    return sorted(r for r in near | set(other) | {M - 1} if 0 <= r < M)
+
+
+# columns enough that each tile height is the cheapest for some number of rows:
+# 64, 128, 192, 256, 320, the last ones with short last tiles
+@pytest.mark.parametrize("M", [200, 1000, 1500, 2000, 2300, 2500])
+@pytest.mark.parametrize("N,K", [(8190, 96), (8192, 1312)])
+def test_matmul_tile_heights(M, N, K):
+    import sparse_moe_ffn_sigmoid_amd as moe
+    announce(f"tile heights {M}x{N}x{K}")
+    xa, xb = operand(M, K, M), operand(N, K, N)
+    pa, pb = moe.mxfp4_pack(xa.cuda()), moe.mxfp4_pack(xb.cuda())
+    rows = sampled_rows(M, (64, 128, 192, 256, 320), M)
+    a, b = mx_round64(as64(xa[rows])), mx_round64(as64(xb))
+    for dt in (F32, BF16, F16):
+        y = moe.mxfp4_matmul(pa["codes"], pa["scales"], pb["codes"], pb["scales"], out_dtype=dt)
+        check_product(y[rows], a, b, dt)
+    index = torch.from_numpy(np.random.default_rng(1).permutation(M).astype(np.int32))
+    index[M // 2] = -1
+    y = moe.mxfp4_matmul(pa["codes"], pa["scales"], pb["codes"], pb["scales"], rows=index.cuda(),
+                         out_dtype=F32)
+    take = index[rows].numpy()
+    a = mx_round64(as64(xa[np.maximum(take, 0)])) * (take >= 0)[:, None]
+    check_product(y[rows], a, b, F32)
+    assert not y[M // 2].any()
+
+
+@pytest.mark.parametrize("lens", [[320, 1, 0, 64, 65, 257, 400, 1293], [300] * 8,
+                                  [0, 0, 1500, 0, 20, 0, 0, 3], [100, 130, 90, 128, 127, 129, 64, 1]])
+def test_groups_tile_heights(lens):
+    import sparse_moe_ffn_sigmoid_amd as moe
+    G, N, K, T = len(lens), 8192, 800, 77
+    announce(f"groups, tile heights {lens}")
+    off = group_offsets(lens, 2)
+    M = int(off[-1]) + 5
+    xt, xb = operand(T, K, 1), operand(G * N, K, 2)
+    pb = moe.mxfp4_pack(xb.view(G, N, K).cuda())
+    index = np.random.default_rng(M).integers(0, T, M).astype(np.int32)
+    out = torch.full((M, N), 9.0, device="cuda")
+    moe.mxfp4_linear(xt.cuda(), pb["codes"], pb["scales"], offsets=dev(off), rows=dev(index),
+                     out_dtype=F32, out=out)
+    a = mx_round64(as64(xt))
+    for g in range(G):
+        rows = [int(off[g]) + r for r in sampled_rows(lens[g], (64, 256, 320), g)] if lens[g] else []
+        if rows:
+            check_product(out[rows], a[index[rows]], mx_round64(as64(xb[g * N:(g + 1) * N])), F32)
+    assert (out[:2] == 9).all() and (out[M - 5:] == 9).all()
+
+
+@pytest.mark.parametrize("M", [700, 1000, 2300])
+def test_kgroup_tile_heights(M):
+    import sparse_moe_ffn_sigmoid_amd as moe
+    N, lens = 4096, [300, 0, 33, 1, 700]
+    off = group_offsets(lens)
+    R = int(off[-1])
+    announce(f"kgroup tile heights {M}")
+    dy, x = operand(R, M, 1), operand(R, N, 2)
+    pd = moe.mxfp4_pack(dy.cuda(), rows=False, cols=True, offsets=dev(off))
+    px = moe.mxfp4_pack(x.cuda(), rows=False, cols=True, offsets=dev(off))
+    for dt in (F32, BF16):
+        dw = moe.mxfp4_matmul_kgroup(pd["codes_t"], pd["scales_t"], px["codes_t"], px["scales_t"],
+                                     offsets=pd["offsets_t"], out_dtype=dt)
+        rows = sampled_rows(M, (64, 128, 192, 256, 320), M)
+        dv, xv = as64(dy)[:, rows], as64(x)
+        for g in range(len(lens)):
+            b, e = off[g], off[g + 1]
+            if e == b:
+                assert not dw[g].any()
+            else:
+                check_product(dw[g][rows], mx_round64(dv[b:e].T), mx_round64(xv[b:e].T), dt)
