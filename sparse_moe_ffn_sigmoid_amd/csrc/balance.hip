@@ -193,10 +193,11 @@ __device__ __forceinline__ float token(const Args& a, int t, const float (&v)[NV
   }
   total = wave_sum(total);
   dot = wave_sum(dot);
-  const float inv = total == 0.f ? 0.f : 1.f / total;
-  const float q = dot * inv;
+  // divided by S_t, not multiplied by 1 / S_t, which overflows under 2^-128
+  const bool none = total == 0.f;
+  const float q = none ? 0.f : dot / total;
   if constexpr (GRAD) {
-    const float g = coef * inv;
+    const float g = none ? 0.f : coef / total;
     float out[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) out[i] = g * (c[i] - q);

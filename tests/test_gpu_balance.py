@@ -331,6 +331,62 @@ def test_balance_rows_beyond_4_gib():
                                                                         device="cuda"))
 
 
+@pytest.mark.parametrize("T", [64, 600])
+def test_balance_scores_near_the_smallest(T):
+    """Rows whose sum's reciprocal overflows fp32 still have shares and gradients."""
+    import sparse_moe_ffn_sigmoid_amd as moe
+    n, k = 32, 4
+    announce(f"balance of tiny scores T={T}")
+    s, idx, off, m = inputs(T, n, k, T)
+    s = np.ldexp(np.round(s * 512) / 512 + 2.0 ** -9, -138).astype(np.float32)  # exact, sums too
+    ref = balance64(s, idx)
+    r = moe.balance_loss(cuda(s), cuda(idx), want_grad=True)
+    # dot = sum c s rounds to whole denormals, 2^-149, at most n times a row
+    extra = n * 2.0 ** -149 / s.sum(1, dtype=np.float64).min()
+    loss, counts, tokens, grad, size = ref
+    row, chain = rounds(T, n)
+    w = n / (k * T * T)
+    assert abs(as64(r["loss"])[0] - loss[0]) <= (row + chain + 2) * U32 * loss[0] + w * T * extra
+    bound = (row + 8) * U32 * size + w / s.sum(1, dtype=np.float64)[:, None] * extra
+    got = as64(r["dscores"])
+    # 1 / S_t is about 2^134 here: a gradient past fp32's largest value is an
+    # infinity of its sign, every other one is that value
+    most = float(torch.finfo(torch.float32).max)
+    sure = np.abs(grad) > most + bound
+    assert (got[sure] == np.sign(grad[sure]) * np.inf).all()
+    fits = np.abs(grad) + bound < most
+    assert fits.any() and (np.abs(got - grad)[fits] <= bound[fits]).all()
+    assert not np.isnan(got).any()
+
+
+def test_router_backward_beyond_4_gib():
+    import sparse_moe_ffn_sigmoid_amd as moe
+    T, d, n = 300032, 7168, 36                              # 4.3 GB of x
+    announce("router backward 300032 x 7168")
+    gen = torch.Generator("cuda").manual_seed(3)
+    x = torch.zeros((T, d), dtype=torch.bfloat16, device="cuda")
+    x[-500:] = torch.randn((500, d), generator=gen, device="cuda").to(torch.bfloat16)
+    w = torch.randn((n, d), generator=gen, device="cuda") * d ** -0.5
+    s = torch.rand((T, n), generator=gen, device="cuda")
+    ds = torch.randn((T, n), generator=gen, device="cuda") * 1e-3
+    r = moe.router_backward(x, w, s, ds)
+    xe, we, se, de = as64(x[-500:]), as64(w), as64(s[-500:]), as64(ds[-500:])
+    g, dx, dw, _ = router64(xe, we, se, de)
+    # the terms of every bound as in test_router_backward
+    ge = np.abs(de) * se * U32 + 3 * U32 * np.abs(g)
+    size = np.abs(g) @ np.abs(we)
+    bx = ge @ np.abs(we) + (3 * 2.0 ** -16 + 3 * (n + 64) * 2.0 ** -23) * size
+    bx = bx + 2.0 ** -8 * (np.abs(dx) + bx) + 1e-38
+    assert (np.abs(as64(r["dx"][-500:]) - dx) <= bx).all()
+    # rows of zeros add nothing: the sum has the last 500 rows' terms, rounded
+    # once more for each part it is split into, at most one per 64 rows
+    bw = ge.T @ np.abs(xe) + 3 * (500 + T // 64) * 2.0 ** -23 * (np.abs(g).T @ np.abs(xe)) + 1e-40
+    assert (np.abs(as64(r["d_w_router"]) - dw) <= bw).all()
+    g = ds.double() * s.double() * (1 - s.double())
+    off = (r["d_router_logit_offset"].double() - g.sum(0)).abs()
+    assert (off <= (3 + 64 + 2) * U32 * ((ds.double() * s.double()).abs().sum(0))).all()
+
+
 def test_balance_refusals_on_the_device():
     import sparse_moe_ffn_sigmoid_amd as moe
     announce("balance refusals")
