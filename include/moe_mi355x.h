@@ -488,7 +488,8 @@ int moe_router_backward(const void* x, const float* w_router, const float* score
  * nearest E2M1 value, ties to the even code, at most 6 in magnitude, as
  * moe_mxfp4_quantize, and the same codes for finite inputs.  A block that
  * holds an infinity or NaN gets scale byte 255 (NaN) and codes 0.  codes and
- * codes_t 16-byte aligned; x aligned to its elements.
+ * codes_t 16-byte aligned; x aligned to its elements.  At most 2^30 rows and
+ * cols and 65535 matrices; with codes_t at most 65535 * 256 padded rows.
  */
 int64_t moe_mxfp4_padded_rows(int64_t rows, int32_t n_groups);
 
@@ -515,7 +516,7 @@ int moe_mxfp4_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, 
  *            i32, non-decreasing, n_groups <= 1024: rows [row_offsets[g],
  *            row_offsets[g + 1]) of C meet matrix g.  Rows of C outside every
  *            group are left as they were.  At most 2^24 rows with groups, 2^30
- *            without
+ *            without; N at most 2^29
  *   row_index [M] i32 or NULL: row r of C is made from row row_index[r] of A,
  *            a_rows >= 1 (an index outside [0, a_rows) makes it a row of
  *            zeros); NULL: row r
@@ -549,7 +550,7 @@ int moe_mxfp4_matmul_kgroup(const uint8_t* a_codes, const uint8_t* a_scales,
  * way: x [x_rows][K] of x_dtype (MOE_F32, MOE_BF16, MOE_F16), rows row_stride
  * elements apart, against packed weights [n_groups][N].  The same bits as
  * moe_mxfp4_pack followed by moe_mxfp4_matmul, up to the order of the sums over
- * K.  A few rows (a token being decoded) are packed in registers, in one launch.
+ * K.  A few rows (a token being decoded) are packed on the way, in one launch.
  *   workspace: >= moe_mxfp4_linear_workspace_bytes(x_rows, K) bytes, 256-byte
  *            aligned.  A few rows without groups need none: NULL is taken, and
  *            MOE_EWORKSPACE returned where the call needs one

@@ -776,6 +776,7 @@ __global__ __launch_bounds__(64 * FUSED_WAVES) void fused_k(MatArgs a, const voi
 // LDS of fused_k's packed rows; it takes what leaves a second block room.
 static int64_t fused_bytes(int64_t M, int64_t K) { return M * (K / 2 + 32 + K / 32); }
 constexpr int64_t FUSED_BYTES = 64 << 10;
+constexpr int64_t FUSED_N = 1 << 26;  // 32 threads a column, fewer than 2^32
 
 template <int DT>
 static int launch_fused(const MatArgs& a, const void* x, int64_t stride, hipStream_t st) {
@@ -873,6 +874,8 @@ static int product(const MatArgs& a, hipStream_t st) {
 
 // Rows of C: tile counts of any row offsets stay within 32 bits.
 constexpr int64_t MAX_ROWS = 1 << 30, MAX_GROUPED_ROWS = 1 << 24;
+// Columns of C: skinny_k's grid has 4 threads a column, fewer than 2^32.
+constexpr int64_t MAX_N = 1 << 29;
 
 static bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
@@ -897,7 +900,8 @@ extern "C" int moe_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales,
   if (M < 0 || N < 1 || K < 32 || K % 32 || a_rows < 0) return MOE_EINVAL;
   if (row_offsets ? n_groups < 1 : n_groups != 1) return MOE_EINVAL;
   if (row_index ? M > 0 && a_rows < 1 : a_rows < M) return MOE_EINVAL;
-  if (M > (row_offsets ? MAX_GROUPED_ROWS : MAX_ROWS) || N > (1 << 30) || a_rows > (1 << 30) || K > (1 << 30) || n_groups > 1024)
+  if (M > (row_offsets ? MAX_GROUPED_ROWS : MAX_ROWS) || N > MAX_N || a_rows > (1 << 30) ||
+      K > (1 << 30) || n_groups > 1024)
     return MOE_EUNSUPPORTED;
   if (M == 0) return MOE_OK;
   const int rc = check_out(out_dtype, out, ld_out, N);
@@ -976,7 +980,8 @@ extern "C" int moe_mxfp4_linear(const void* x, int32_t x_dtype, int64_t x_rows,
   if (row_offsets ? n_groups < 1 : n_groups != 1) return MOE_EINVAL;
   if (row_index ? M > 0 && x_rows < 1 : x_rows < M) return MOE_EINVAL;
   if (x_dtype != MOE_F32 && x_dtype != MOE_BF16 && x_dtype != MOE_F16) return MOE_EUNSUPPORTED;
-  if (M > (row_offsets ? MAX_GROUPED_ROWS : MAX_ROWS) || N > (1 << 30) || x_rows > (1 << 30) || K > (1 << 30) || n_groups > 1024)
+  if (M > (row_offsets ? MAX_GROUPED_ROWS : MAX_ROWS) || N > MAX_N || x_rows > (1 << 30) ||
+      K > (1 << 30) || n_groups > 1024)
     return MOE_EUNSUPPORTED;
   if (row_stride > (int64_t(1) << 56) / (x_rows + 1)) return MOE_EINVAL;
   if (M == 0) return MOE_OK;
@@ -988,8 +993,8 @@ extern "C" int moe_mxfp4_linear(const void* x, int32_t x_dtype, int64_t x_rows,
     return MOE_EINVAL;
   if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MOE_EINVAL;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (!row_offsets && M <= 16 && fused_bytes(M, K) <= FUSED_BYTES && aligned16(x) &&
-      row_stride * size % 16 == 0) {
+  if (!row_offsets && M <= 16 && N <= FUSED_N && fused_bytes(M, K) <= FUSED_BYTES &&
+      aligned16(x) && row_stride * size % 16 == 0) {
     MatArgs a{};
     a.B = w_codes;
     a.Bs = w_scales;

@@ -321,7 +321,7 @@ extern "C" int moe_mxfp4_pack(const void* x, int32_t dtype, int64_t batch, int64
       n_groups > 1024)
     return MOE_EUNSUPPORTED;
   const int64_t padded = moe_mxfp4_padded_rows(rows, n_groups);
-  if (codes_t && (padded + 127) / 128 > 65535) return MOE_EUNSUPPORTED;
+  if (codes_t && (padded + PACK_ROWS - 1) / PACK_ROWS > 65535) return MOE_EUNSUPPORTED;
   if (row_stride > (int64_t(1) << 56) / (rows + 1) ||
       batch_stride > (int64_t(1) << 56) / (batch + 1))
     return MOE_EINVAL;

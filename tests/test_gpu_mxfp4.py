@@ -483,6 +483,21 @@ def test_output_beyond_32_bits():
     check_product(y[rows][:, -300:], mx_round64(as64(x[rows])), mx_round64(as64(w[-300:])), BF16)
 
 
+def test_linear_of_very_many_columns():
+    """More columns than one launch has threads for at 32 a column."""
+    import sparse_moe_ffn_sigmoid_amd as moe
+    N, K = (1 << 27) + 48, 32                      # 2.1 GB of codes
+    announce("2^27 columns")
+    codes = torch.zeros((N, K // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.full((N, 1), 127, dtype=torch.uint8, device="cuda")
+    codes[-100:] = random_codes(100, K // 2)
+    x = operand(2, K, 1)
+    y = moe.mxfp4_linear(x.cuda(), codes, scales, out_dtype=F32)
+    b = mx_decode64(nibbles(codes[-100:]), scales[-100:].cpu().numpy())
+    check_product(y[:, -100:], mx_round64(as64(x)), b, F32)
+    assert not y[:, :1000].any()
+
+
 def test_products_on_two_streams_and_given_buffers():
     import sparse_moe_ffn_sigmoid_amd as moe
     N, K = 300, 512
