@@ -647,6 +647,8 @@ def latent_backward(shape: MoeShape, weights: dict, x: torch.Tensor, scores: tor
     _check(scores, "scores", torch.float32, (T, n), dev)
     _check(idx, "idx", torch.int32, (T, k), dev)
     _check(w, "w", torch.float32, (T, k), dev)
+    if dscores is not None:  # refused before anything runs
+        _check(dscores, "dscores", torch.float32, (T, n), dev)
     wts = MoeWeights(*[None if weights.get(f) is None else weights[f].data_ptr()
                        for f, _ in MoeWeights._fields_])
     out = {"dx": torch.empty((T, d), dtype=torch.bfloat16, device=dev)}
@@ -728,6 +730,8 @@ def latent_backward_train(shape: MoeShape, weights: dict, x: torch.Tensor, score
     _check(scores, "scores", torch.float32, (T, n), dev)
     _check(idx, "idx", torch.int32, (T, k), dev)
     _check(w, "w", torch.float32, (T, k), dev)
+    if dscores is not None:  # refused before anything runs
+        _check(dscores, "dscores", torch.float32, (T, n), dev)
     _check(saved, "saved", torch.uint8, (saved.numel(),), dev)
     wts = MoeWeights(*[None if weights.get(f) is None else weights[f].data_ptr()
                        for f, _ in MoeWeights._fields_])

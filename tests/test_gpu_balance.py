@@ -304,6 +304,9 @@ def test_balance_loss_in_a_training_step():
                                    dscores=b["dscores"])
     want = as64(both["d_w_router"])
     assert np.linalg.norm(as64(tr["d_w_router"]) - want) <= 1e-2 * np.linalg.norm(want)
+    for bad in (b["dscores"].double(), b["dscores"][:, :-1], b["dscores"].cpu()):
+        with pytest.raises(ValueError):
+            moe.latent_backward(sh, w, x, f["scores"], f["idx"], f["w"], dout, dscores=bad)
     with pytest.raises(ValueError):
         moe.latent_backward_train(sh, w, x, f2["scores"], f2["idx"], f2["w"], dout, saved, lr=0.1,
                                   dscores=b["dscores"])
